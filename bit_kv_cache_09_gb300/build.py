@@ -1,8 +1,8 @@
 """Build libkvq.so (CUDA, sm_103a) in-tree with nvcc.
 
 ``python -m bit_kv_cache_09_gb300.build`` compiles every ``csrc/*.cu`` file in
-parallel and links ``libkvq.so`` next to this file. The quantizer translation
-unit is compiled with ``-fmad=false`` so that no multiply-add is contracted.
+parallel and links ``libkvq.so`` next to this file. The quantizers' translation
+units are compiled with ``-fmad=false`` so that no multiply-add is contracted.
 """
 
 from __future__ import annotations
@@ -19,7 +19,7 @@ OBJ = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libkvq.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
-PER_FILE = {"kvq_quant.cu": ["-fmad=false"]}
+PER_FILE = {"kvq_quant.cu": ["-fmad=false"], "kvq_paged_quant.cu": ["-fmad=false"]}
 
 
 def nvcc() -> str:

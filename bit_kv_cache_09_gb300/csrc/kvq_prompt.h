@@ -1,0 +1,26 @@
+// kvq_prompt.h — launch description of the prompt attention (library-internal).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/kvq.h"
+
+namespace kvq {
+
+struct PromptParams {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  float* lse;
+  const int32_t *q_start, *kv_start;
+  int64_t q_stride, k_stride, v_stride, out_stride;  // elements
+  int32_t n_q, n_kv, n_seqs, H, r, causal, zero_rest;
+  float scale_log2;
+  uint32_t* err;
+  uint64_t wait_ns;
+};
+
+cudaError_t launch_prompt(const PromptParams& p, int dtype, cudaStream_t stream);
+
+}  // namespace kvq

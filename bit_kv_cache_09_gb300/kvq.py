@@ -27,7 +27,16 @@ DECODE_ERR_WAIT_TIMEOUT = 1  # bit of the decode error word
 EXPORTED = ("kvq_buffer_sizes", "kvq_quantize_append", "kvq_dequantize", "kvq_decode_workspace_size",
             "kvq_decode_attention", "kvq_decode_attention_impl", "kvq_decode_num_splits", "kvq_status_string",
             "kvq_version", "kvq_decode_attention_noalloc", "kvq_decode_step", "kvq_decode_attention_ex",
-            "kvq_decode_step_ex", "kvq_decode_error", "kvq_decode_noalloc_error")
+            "kvq_decode_step_ex", "kvq_decode_error", "kvq_decode_noalloc_error", "kvq_paged_buffer_sizes",
+            "kvq_paged_step_tables", "kvq_paged_append", "kvq_paged_dequantize", "kvq_paged_workspace_size",
+            "kvq_paged_decode_attention", "kvq_prompt_attention")
+PAGED_FORMATS = {"int8": 0, "e4m3": 1}  # kvq_paged_config.format
+F16, BF16 = 0, 1  # 16-bit types of the paged cache and of the prompt attention
+PAGED_ERR_NEW, PAGED_ERR_LENGTH, PAGED_ERR_BLOCKS, PAGED_ERR_STATE = 1, 2, 4, 8  # bits of step.status[0]
+PAGED_ERR_ROWS, PAGED_ERR_TABLE = 16, 32
+PAGED_ERR_NAMES = {1: "new_tokens below -1 or more than max_new in all", 2: "a request outgrows max_blocks",
+                   4: "not enough free blocks", 8: "lengths or free count out of range",
+                   16: "fewer key/value rows than the step's new tokens", 32: "a block number outside the pool"}
 
 
 class KVQError(RuntimeError):
@@ -45,6 +54,15 @@ class KVQDeviceError(RuntimeError):
         self.word = word
 
 
+class KVQStepError(RuntimeError):
+    """A step of the paged cache recorded an error (bits PAGED_ERR_* of its status word)."""
+
+    def __init__(self, bits: int):
+        names = [n for bit, n in PAGED_ERR_NAMES.items() if bits & bit]
+        super().__init__(f"step status 0x{bits:x}: {'; '.join(names) or 'unknown bits'}")
+        self.bits = bits
+
+
 class kvq_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "batch", "n_kv_heads", "gqa_ratio", "d_head",
                                                "max_seq_len", "bits", "k_group", "v_group", "residual_len",
@@ -53,6 +71,33 @@ class kvq_config(ctypes.Structure):
 
 class kvq_buffers(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in BUFFER_NAMES]
+
+
+class kvq_paged_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "n_kv_heads", "gqa_ratio", "d_head", "n_blocks",
+                                               "block_tokens", "n_requests", "max_blocks", "max_new", "format",
+                                               "dtype")]
+
+
+class kvq_paged_buffers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "tails")]
+
+
+class kvq_paged_state(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("lens", "block_table", "free_list", "free_count")]
+
+
+class kvq_paged_step(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("lens", "free_count", "q_start", "positions", "slots", "units",
+                                               "tile_start", "status")]
+
+
+class kvq_prompt_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_kv_heads", "gqa_ratio", "d_head", "dtype", "n_seqs", "causal", "zero_rest")]
+                + [(n, ctypes.c_int64) for n in ("n_q", "n_kv")] + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+                + [(n, ctypes.c_void_p) for n in ("q_start", "kv_start")] + [("softmax_scale", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("out", "lse")])
 
 
 _lib = None
@@ -99,6 +144,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.kvq_decode_noalloc_error.restype = ctypes.c_int
         L.kvq_decode_num_splits.argtypes = [cfgp, ctypes.c_int64]
         L.kvq_decode_num_splits.restype = ctypes.c_int32
+        pcfg, pbuf, pstep = (ctypes.POINTER(t) for t in (kvq_paged_config, kvq_paged_buffers, kvq_paged_step))
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        L.kvq_paged_buffer_sizes.argtypes = [pcfg, ctypes.POINTER(ctypes.c_size_t)]
+        L.kvq_paged_buffer_sizes.restype = ctypes.c_int
+        L.kvq_paged_step_tables.argtypes = [pcfg, ctypes.POINTER(kvq_paged_state), vp, pstep, i32, vp]
+        L.kvq_paged_step_tables.restype = ctypes.c_int
+        L.kvq_paged_append.argtypes = [pcfg, pbuf, vp, pstep, i32, i64, vp, i64, vp, i64, vp]
+        L.kvq_paged_append.restype = ctypes.c_int
+        L.kvq_paged_dequantize.argtypes = [pcfg, pbuf, i32, i64, vp, vp, vp, vp]
+        L.kvq_paged_dequantize.restype = ctypes.c_int
+        L.kvq_paged_workspace_size.argtypes = [pcfg]
+        L.kvq_paged_workspace_size.restype = ctypes.c_size_t
+        L.kvq_paged_decode_attention.argtypes = [pcfg, pbuf, vp, pstep, i32, vp, i64, ctypes.c_float, vp, i32,
+                                                 vp, ctypes.c_size_t, vp]
+        L.kvq_paged_decode_attention.restype = ctypes.c_int
+        L.kvq_prompt_attention.argtypes = [ctypes.POINTER(kvq_prompt_args), vp, ctypes.c_size_t, vp]
+        L.kvq_prompt_attention.restype = ctypes.c_int
         L.kvq_status_string.argtypes = [ctypes.c_int]
         L.kvq_status_string.restype = ctypes.c_char_p
         L.kvq_version.argtypes = []
@@ -214,3 +276,52 @@ def kvq_decode_noalloc_error(stream: int = 0) -> int:
     word = ctypes.c_uint32(0)
     _check("kvq_decode_noalloc_error", load().kvq_decode_noalloc_error(stream, ctypes.byref(word)))
     return int(word.value)
+
+
+def make_paged_config(*, n_layers, n_kv_heads, gqa_ratio, d_head, n_blocks, block_tokens, n_requests, max_blocks,
+                      max_new, fmt, dtype) -> kvq_paged_config:
+    """fmt: a key of PAGED_FORMATS (or its number); dtype: F16 or BF16."""
+    return kvq_paged_config(n_layers, n_kv_heads, gqa_ratio, d_head, n_blocks, block_tokens, n_requests, max_blocks,
+                            max_new, PAGED_FORMATS.get(fmt, fmt), dtype)
+
+
+def kvq_paged_buffer_sizes(cfg: kvq_paged_config) -> list[int]:
+    out = (ctypes.c_size_t * 3)()
+    _check("kvq_paged_buffer_sizes", load().kvq_paged_buffer_sizes(ctypes.byref(cfg), out))
+    return [int(v) for v in out]
+
+
+def kvq_paged_workspace_size(cfg: kvq_paged_config) -> int:
+    return int(load().kvq_paged_workspace_size(ctypes.byref(cfg)))
+
+
+def kvq_paged_step_tables(cfg: kvq_paged_config, state: kvq_paged_state, new_tokens: int, step: kvq_paged_step,
+                          commit: int = 1, stream: int = 0) -> None:
+    _check("kvq_paged_step_tables", load().kvq_paged_step_tables(ctypes.byref(cfg), ctypes.byref(state), new_tokens,
+                                                                 ctypes.byref(step), commit, stream))
+
+
+def kvq_paged_append(cfg: kvq_paged_config, bufs: kvq_paged_buffers, block_table: int, step: kvq_paged_step,
+                     layer: int, n_rows: int, k: int, k_stride: int, v: int, v_stride: int, stream: int = 0) -> None:
+    _check("kvq_paged_append", load().kvq_paged_append(ctypes.byref(cfg), ctypes.byref(bufs), block_table,
+                                                       ctypes.byref(step), layer, n_rows, k, k_stride, v, v_stride,
+                                                       stream))
+
+
+def kvq_paged_dequantize(cfg: kvq_paged_config, bufs: kvq_paged_buffers, layer: int, n: int, slots: int, k_out: int,
+                         v_out: int, stream: int = 0) -> None:
+    _check("kvq_paged_dequantize", load().kvq_paged_dequantize(ctypes.byref(cfg), ctypes.byref(bufs), layer, n, slots,
+                                                               k_out, v_out, stream))
+
+
+def kvq_paged_decode_attention(cfg: kvq_paged_config, bufs: kvq_paged_buffers, block_table: int, step: kvq_paged_step,
+                               layer: int, q: int, q_stride: int, softmax_scale: float, out: int, zero_rest: int,
+                               ws: int, ws_bytes: int, stream: int = 0) -> None:
+    _check("kvq_paged_decode_attention",
+           load().kvq_paged_decode_attention(ctypes.byref(cfg), ctypes.byref(bufs), block_table, ctypes.byref(step),
+                                             layer, q, q_stride, softmax_scale, out, zero_rest, ws, ws_bytes,
+                                             stream))
+
+
+def kvq_prompt_attention(args: kvq_prompt_args, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    _check("kvq_prompt_attention", load().kvq_prompt_attention(ctypes.byref(args), ws, ws_bytes, stream))

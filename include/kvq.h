@@ -287,6 +287,178 @@ kvq_status kvq_decode_noalloc_error(void* stream, uint32_t* err_out);
  * config. */
 int32_t kvq_decode_num_splits(const kvq_config* cfg, int64_t s_cur);
 
+/* ---- Paged 8-bit cache: requests of different lengths --------------------------------
+ *
+ * The cache above gives every sequence of a batch the same length and its own contiguous
+ * memory. Here the tokens of each request live in blocks of block_tokens tokens taken
+ * from a pool, and every request has its own length.
+ *
+ * Quantizer (one scale per block, kv head and tensor; symmetric, 8 bits)
+ *   amax = max|x| over the block's block_tokens x d_head entries of a head; in binary32,
+ *   round to nearest even: scale = max(amax / top, 2^-126), or 1 when amax = 0, with
+ *   top = 127 (KVQ_PAGED_INT8) or 448 (KVQ_PAGED_E4M3); y = x / scale;
+ *   int8: q = clamp(rint(y), -127, 127), stored as q + 128; e4m3: q = y rounded to the
+ *   nearest e4m3 value (ties to even, saturating). x_hat = scale * q. A block that holds
+ *   an infinity or a NaN in a head gets the scale NaN for that head and tensor, so that
+ *   whatever reads it is NaN instead of silently wrong; other blocks and heads are not
+ *   affected.
+ *   A block is quantized when its last token arrives. The tokens of a request's unfinished
+ *   block are 16-bit copies in the request's tail row, so that the cache state depends
+ *   only on the tokens, never on how they were split into steps.
+ *
+ * Memory (device, owned by the caller, 256-byte aligned, zero-filled before first use)
+ *   codes  : [n_layers][n_blocks][n_kv_heads][block_tokens / 32] tiles of 8192 bytes (32
+ *            tokens: 4096 bytes of key codes, then 4096 of value codes)
+ *   scales : [n_layers][n_blocks][n_kv_heads][2] binary32 (key scale, value scale)
+ *   tails  : [n_layers][n_requests][n_kv_heads][block_tokens / 16] tiles of 8192 bytes (16
+ *            tokens: 2048 key entries of 16 bits, then 2048 value entries)
+ *   Inside a tile the entries are in the order in which the lanes of the decode kernel's
+ *   matrix products hold them (bit_kv_cache_09_gb300/csrc/kvq_paged.cuh has the index
+ *   functions); kvq_paged_dequantize reads any token back.
+ *
+ * A step of a serving loop: kvq_paged_step_tables once, then per layer kvq_paged_append
+ * and kvq_paged_decode_attention (or kvq_prompt_attention for prompts). No call
+ * synchronizes or reads lengths on the host: all of them come from device memory, so a
+ * step can be captured in a CUDA graph and replayed. */
+enum { KVQ_PAGED_INT8 = 0, KVQ_PAGED_E4M3 = 1 }; /* kvq_paged_config.format */
+enum { KVQ_F16 = 0, KVQ_BF16 = 1 };              /* 16-bit types of keys, values, queries and outputs */
+
+/* Supported: d_head == 128; 1 <= gqa_ratio <= 8; 1 <= n_kv_heads <= 255; block_tokens in
+ * {32, 64, 128}; 1 <= n_requests <= 8192; n_layers, n_blocks, max_blocks and max_new >= 1;
+ * n_blocks * block_tokens, n_requests * block_tokens, (max_blocks + 1) * block_tokens and
+ * max_new < 2^31 - 2^16; n_requests * (max_blocks + 1) * n_kv_heads * (block_tokens / 16)
+ * < 2^40. */
+typedef struct {
+  int32_t n_layers;
+  int32_t n_kv_heads;
+  int32_t gqa_ratio;    /* query heads per kv head */
+  int32_t d_head;
+  int32_t n_blocks;     /* pool blocks of each layer */
+  int32_t block_tokens; /* tokens of a block */
+  int32_t n_requests;   /* request rows */
+  int32_t max_blocks;   /* finished blocks a request can have; it holds at most
+                           (max_blocks + 1) * block_tokens - 1 tokens */
+  int32_t max_new;      /* tokens one step can add, over all requests */
+  int32_t format;       /* KVQ_PAGED_* */
+  int32_t dtype;        /* KVQ_F16 or KVQ_BF16 */
+} kvq_paged_config;
+
+typedef struct {
+  void* codes;
+  float* scales;
+  void* tails;
+} kvq_paged_buffers;
+
+/* What is known of the requests between steps (device, 4-byte aligned). */
+typedef struct {
+  int32_t* lens;        /* [n_requests] tokens cached; 0 to start with */
+  int32_t* block_table; /* [n_requests][max_blocks] pool block of each finished block */
+  int32_t* free_list;   /* [n_blocks] the first free_count entries are the free blocks, a stack */
+  int32_t* free_count;  /* [1] */
+} kvq_paged_state;
+
+/* What kvq_paged_step_tables writes for one step and the calls of its layers read (device,
+ * 4-byte aligned, units 8-byte). Zero-fill `status` once. */
+typedef struct {
+  int32_t* lens;        /* [n_requests] tokens after the step */
+  int32_t* free_count;  /* [1] free blocks after the step */
+  int32_t* q_start;     /* [n_requests + 1] first packed row of each request's new tokens */
+  int32_t* positions;   /* [max_new] position of each new token in its request */
+  int32_t* slots;       /* [max_new] where each new token is kept: block * block_tokens + offset once
+                           its block is finished, -1 - (request * block_tokens + offset) in a tail */
+  int32_t* units;       /* [max_new / block_tokens + n_requests][2] work list of the append */
+  int32_t* tile_start;  /* [n_requests + 1] work of the decode attention */
+  uint32_t* status;     /* [4] error bits (KVQ_PAGED_ERR_*), number of units, then private */
+} kvq_paged_step;
+
+/* Error bits of step.status[0]. A step with one of the first four is refused as a whole: it
+ * becomes a step without new tokens. The bits stay set until the caller clears them. */
+#define KVQ_PAGED_ERR_NEW 1u     /* an entry of new_tokens below -1, or a sum above max_new */
+#define KVQ_PAGED_ERR_LENGTH 2u  /* a request would outgrow max_blocks */
+#define KVQ_PAGED_ERR_BLOCKS 4u  /* not enough free blocks */
+#define KVQ_PAGED_ERR_STATE 8u   /* lens or free_count out of range */
+#define KVQ_PAGED_ERR_ROWS 16u   /* append: fewer rows than the step's new tokens (those rows are skipped) */
+#define KVQ_PAGED_ERR_TABLE 32u  /* append, attention: a block number outside the pool (not accessed) */
+
+enum { KVQ_PAGED_BUF_CODES = 0, KVQ_PAGED_BUF_SCALES = 1, KVQ_PAGED_BUF_TAILS = 2, KVQ_PAGED_NUM_BUFFERS = 3 };
+
+/* Sizes in bytes of the three buffers. */
+kvq_status kvq_paged_buffer_sizes(const kvq_paged_config* cfg, size_t bytes[KVQ_PAGED_NUM_BUFFERS]);
+
+/* Builds the tables of a step from request lengths. new_tokens [n_requests] (device):
+ * tokens the step adds to each request, 0 for none, -1 for a request that is done: its
+ * blocks return to the free stack and its length becomes 0. Released blocks are pushed in
+ * row order, then the blocks that the step's tokens finish are popped in row order. With
+ * commit != 0 state.lens and state.free_count become those after the step; with commit
+ * == 0 they stay, and the same step can be built again (block-table entries and free-list
+ * entries beyond what they count are written either way). One launch. */
+kvq_status kvq_paged_step_tables(const kvq_paged_config* cfg, const kvq_paged_state* state, const int32_t* new_tokens,
+                                 const kvq_paged_step* step, int32_t commit, void* stream);
+
+/* Stores the step's new tokens of one layer. k, v: device rows of the config's dtype, new
+ * token i of the packed order (step.q_start) at element i * k_stride, its heads of d_head
+ * entries behind one another; n_rows rows may be read (rows beyond the step's tokens are
+ * not). 16-byte aligned, strides multiples of 8 elements. */
+kvq_status kvq_paged_append(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs, const int32_t* block_table,
+                            const kvq_paged_step* step, int32_t layer, int64_t n_rows, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, void* stream);
+
+/* Reads tokens back as binary32: row i of k_out and v_out [n][n_kv_heads][d_head] (16-byte
+ * aligned) is the token kept at slots[i] (device; the encoding of step.slots). A slot
+ * outside the cache gives a row of NaN. n may be 0. */
+kvq_status kvq_paged_dequantize(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs, int32_t layer, int64_t n,
+                                const int32_t* slots, float* k_out, float* v_out, void* stream);
+
+/* Bytes of workspace of kvq_paged_decode_attention (0 for a bad config): an error word
+ * (first 4 bytes, kvq_decode_error reads it), counters and partial results. Zero-fill it
+ * once; every call leaves its counters at zero. Calls that may overlap need one each. */
+size_t kvq_paged_workspace_size(const kvq_paged_config* cfg);
+
+/* Decode attention of one layer for the newest token of every request with new tokens in the
+ * step: out[i][h] = softmax(softmax_scale * q[i][h] . k_hat[t]) * v_hat[t] over the
+ * step.lens[i] tokens of request i and kv head h / gqa_ratio, with the codes and scales
+ * of finished blocks and the 16-bit rows of the tail. q: row i at element i * q_stride
+ * (16-byte aligned, a multiple of 8), its n_kv_heads * gqa_ratio heads behind one another;
+ * out [n_requests][n_kv_heads * gqa_ratio][d_head] in the config's dtype (16-byte
+ * aligned). Rows of requests without new tokens are left as they were, or, with zero_rest != 0,
+ * filled with zeros. */
+kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs,
+                                      const int32_t* block_table, const kvq_paged_step* step, int32_t layer,
+                                      const void* q, int64_t q_stride, float softmax_scale, void* out,
+                                      int32_t zero_rest, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Attention of whole prompts, packed one behind the other ------------------------- */
+
+/* Sequence s has queries q_start[s] .. q_start[s+1] - 1 and keys kv_start[s] ..
+ * kv_start[s+1] - 1 (device arrays of n_seqs + 1, not decreasing, within the rows given;
+ * kv_start may be the same array). With causal != 0 the last query of a sequence sees its
+ * last key, the query before it one key less, and so on; a query that sees no key gets
+ * zeros and lse -inf. Element (token, head, c) of q, k, v and out is at token * stride +
+ * head * d_head + c; strides are multiples of 8 elements, at least a row of heads and below
+ * 2^31, pointers 16-byte aligned, and out and lse rows that belong to no sequence are left as they were (with
+ * zero_rest != 0: filled with zeros, lse -inf). Values
+ * of one sequence never reach the outputs of another, whatever they are.
+ * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
+ * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale finite and >= 0. */
+typedef struct {
+  int32_t n_kv_heads, gqa_ratio, d_head;
+  int32_t dtype;  /* KVQ_F16 or KVQ_BF16: q, k, v and out */
+  int32_t n_seqs;
+  int32_t causal;
+  int32_t zero_rest;
+  int64_t n_q, n_kv;                                /* rows of q / out / lse, rows of k / v */
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride, out_stride; /* elements from one token to the next */
+  const int32_t *q_start, *kv_start;
+  float softmax_scale;
+  void* out;
+  float* lse; /* NULL, or [n_q][n_kv_heads * gqa_ratio]: ln sum exp(softmax_scale * q . k) */
+} kvq_prompt_args;
+
+/* ws: at least 256 bytes of device memory, zero-filled once (error word in its first 4
+ * bytes, kvq_decode_error reads it). */
+kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* ws, size_t ws_bytes, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* kvq_status_string(kvq_status status);
 
