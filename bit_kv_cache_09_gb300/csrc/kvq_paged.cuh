@@ -70,6 +70,9 @@ inline kvq_status make_paged_geometry(const kvq_paged_config* c, PagedGeometry* 
   if (c->n_blocks * bt >= lim || c->n_requests * bt >= lim || (int64_t(c->max_blocks) + 1) * bt >= lim ||
       c->max_new >= lim)
     return KVQ_ERR_UNSUPPORTED;
+  // decode tiles of a layer are counted in 32 bits (each is 8 KB of memory per layer)
+  if ((c->n_blocks * bt / kTileCodeTokens + c->n_requests * bt / kTileTailTokens) * c->n_kv_heads >= lim)
+    return KVQ_ERR_UNSUPPORTED;
   if (int64_t(c->n_requests) * (int64_t(c->max_blocks) + 1) >= (int64_t(1) << 40) / (c->n_kv_heads * (bt / 16)))
     return KVQ_ERR_UNSUPPORTED;
   PagedGeometry x;
@@ -159,6 +162,13 @@ cudaError_t launch_paged_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_paged_append(const PagedAppendParams& p, int64_t max_units, int fmt, int dtype, cudaStream_t stream);
 cudaError_t launch_paged_dequant(const PagedDequantParams& p, int fmt, int dtype, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int fmt, int dtype, cudaStream_t stream);
+
+// Workspace of the decode attention: error word at 0, tickets [R * H] at 256, then partial
+// results.
+constexpr size_t kPagedTickets = 256;
+inline size_t paged_workspace_parts(const PagedGeometry& g) {
+  return kPagedTickets + ((size_t)g.R * g.H * 4 + 255) / 256 * 256;
+}
 size_t paged_workspace_bytes(const PagedGeometry& g);
 
 }  // namespace kvq

@@ -176,8 +176,8 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   p.max_blocks = g.max_blocks;
   p.n_blocks = g.n_blocks;
   p.err = static_cast<uint32_t*>(ws);
-  p.tickets = nullptr;
-  p.parts = nullptr;
+  p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kvq::kPagedTickets);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kvq::paged_workspace_parts(g));
   p.wait_ns = kvq::kDefaultWaitNs;
   return of(kvq::launch_paged_decode(p, g.fmt, g.dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -327,7 +327,8 @@ enum { KVQ_F16 = 0, KVQ_BF16 = 1 };              /* 16-bit types of keys, values
  * {32, 64, 128}; 1 <= n_requests <= 8192; n_layers, n_blocks, max_blocks and max_new >= 1;
  * n_blocks * block_tokens, n_requests * block_tokens, (max_blocks + 1) * block_tokens and
  * max_new < 2^31 - 2^16; n_requests * (max_blocks + 1) * n_kv_heads * (block_tokens / 16)
- * < 2^40. */
+ * < 2^40; (n_blocks * block_tokens / 32 + n_requests * block_tokens / 16) * n_kv_heads < 2^31 -
+ * 2^16. */
 typedef struct {
   int32_t n_layers;
   int32_t n_kv_heads;
