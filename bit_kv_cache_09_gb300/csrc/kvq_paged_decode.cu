@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_kernels.h"
 #include "kvq_paged.cuh"
@@ -113,18 +114,57 @@ struct TileInfo {
   float ks, vs;
 };
 
-__device__ __forceinline__ TileInfo tile_info(const PagedDecodeParams& p, int x, int end) {
+// 32 request rows from `row` on, one per lane: where their tiles start and how long they are.
+struct RowWindow {
+  int row, start, len;
+};
+
+__device__ __forceinline__ RowWindow row_window(const PagedDecodeParams& p, int row) {
+  const int i = min(row + (int)(threadIdx.x & 31), p.R);
+  return RowWindow{row, p.tile_start[i], p.lens[min(i, p.R - 1)]};
+}
+
+// One round of a search for the last row of lo .. hi - 1 whose tiles start at or before v, with
+// tile_start[lo] <= v < tile_start[hi]: 32 samples, lane i holding sample i, leave 1/32 of the rows.
+__device__ __forceinline__ int search_step(int lo, int hi) { return (hi - lo + 31) >> 5; }
+__device__ __forceinline__ void narrow(int& lo, int& hi, int v, int sample) {
+  const int step = search_step(lo, hi), i = lo + (int)(threadIdx.x & 31) * step;
+  lo += (__popc(__ballot_sync(0xffffffffu, i < hi && sample <= v)) - 1) * step;
+  hi = min(lo + step, hi);
+}
+
+// Moves the window up to at most 31 rows before the row of tile v (all lanes, the same v).
+__device__ __forceinline__ void seek(const PagedDecodeParams& p, RowWindow& w, int lo, int hi, int v) {
+  while (hi - lo > 31) narrow(lo, hi, v, p.tile_start[min(lo + (int)(threadIdx.x & 31) * search_step(lo, hi), hi)]);
+  w = row_window(p, lo);
+}
+
+// Tile x of the list for every lane with x < end (all lanes call it, with rising x).
+__device__ __forceinline__ TileInfo tile_info(const PagedDecodeParams& p, RowWindow& w, int x, int end) {
   TileInfo ti{nullptr, -1, 32, 0, 0.0f, 0.0f};
-  if (x >= end) return ti;
-  const int v = x / p.H;
-  int lo = 0, hi = p.R;  // tile_start[lo] <= v < tile_start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.tile_start[mid] <= v) lo = mid; else hi = mid;
+  const int v = min(x, end - 1) / p.H;
+  int row = 0, t0 = 0, t1 = 1, len = 0;
+  for (bool todo = x < end;;) {
+    int k = 0;  // last row of the window that starts at or before v
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+      if (__shfl_sync(0xffffffffu, w.start, k + step) <= v) k += step;
+    const int a = __shfl_sync(0xffffffffu, w.start, k), b = __shfl_sync(0xffffffffu, w.start, min(k + 1, 31));
+    const int c = __shfl_sync(0xffffffffu, w.len, k);
+    if (todo && k < 31) {  // the row and the next one's start are in the window
+      row = w.row + k;
+      t0 = a;
+      t1 = b;
+      len = c;
+      todo = false;
+    }
+    const uint32_t left = __ballot_sync(0xffffffffu, todo);
+    if (!left) break;
+    seek(p, w, w.row + 31, p.R, __shfl_sync(0xffffffffu, v, __ffs(left) - 1));
   }
-  const int row = lo, t0 = p.tile_start[row], nt = p.tile_start[row + 1] - t0;
-  const int rem = x - t0 * p.H, h = rem / nt, t = rem - h * nt;
-  const int len = p.lens[row], full = len / p.bt, per = p.bt / kTileCodeTokens;
+  if (x >= end) return ti;
+  const int nt = t1 - t0, rem = x - t0 * p.H, h = rem / nt, t = rem - h * nt;
+  const int full = len / p.bt, per = p.bt / kTileCodeTokens;
   ti.pair = row * p.H + h;
   ti.flags = (t == 0 ? 1 : 0) | (t == nt - 1 ? 2 : 0);
   if (t < full * per) {
@@ -167,6 +207,14 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
+// Counts the CTA in at its pair. The release covers what the CTA's other threads wrote before the
+// barrier in front, the acquire what the CTAs counted before wrote.
+__device__ __forceinline__ uint32_t take_ticket(uint32_t* ticket) {
+  uint32_t n;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
+  return n;
+}
+
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const PagedDecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -184,6 +232,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
   pdl_allow_dependents();
 
   const int H = p.H, r = p.r;
+  // one round trip: the number of tiles, and the first rows or samples of the search for this warp's row
+  RowWindow window = row_window(p, 0);
+  const int sample = p.tile_start[min(lane * search_step(0, p.R), p.R)];
   const int total = p.tile_start[p.R] * H;
   // at least one tile per warp, so that short lists need no joining across CTAs
   const int ctas = max(1, min((int)gridDim.x, total / kWarps));
@@ -199,13 +250,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
   const int a_cta = (int)((int64_t)total * cta / ctas), b_cta = (int)((int64_t)total * (cta + 1) / ctas);
   const int x_beg = a_cta + (b_cta - a_cta) * warp / kWarps, x_end = a_cta + (b_cta - a_cta) * (warp + 1) / kWarps;
 
-  TileInfo next = tile_info(p, x_beg + lane, x_end), cur = next;
+  if (p.R > 31 && x_beg < x_end) {
+    int lo = 0, hi = p.R;
+    narrow(lo, hi, x_beg / H, sample);
+    seek(p, window, lo, hi, x_beg / H);
+  }
+  TileInfo next = tile_info(p, window, x_beg + lane, x_end), cur = next;
   int issue = x_beg, next_base = x_beg, cur_base = x_beg;
   bool dead = false;  // a wait ran out: no more copies, the bookkeeping goes on
   auto issue_one = [&]() {  // starts the copy of tile `issue`
     if (issue - next_base == 32) {
       next_base = issue;
-      next = tile_info(p, issue + lane, x_end);
+      next = tile_info(p, window, issue + lane, x_end);
+    }
+    const int first_of = __shfl_sync(0xffffffffu, next.flags, issue - next_base) & 1;
+    if (first_of || issue == x_beg) {  // the pair's queries are wanted soon
+      const int pr = __shfl_sync(0xffffffffu, next.pair, issue - next_base);
+      if (lane < 2 * r) {
+        const int row = pr / H, h = pr - row * H;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + (int64_t)row * p.q_stride + h * r * kPagedDim + lane * 64));
+      }
     }
     const uint64_t src = __shfl_sync(0xffffffffu, (uint64_t)(uintptr_t)next.src, issue - next_base);
     const int s = (issue - x_beg) % kStages;
@@ -460,6 +524,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
   // Join the parts of this CTA. They follow one another as head and tail parts of warps 0, 1,
   // ...; neighbours of the same pair form a group. Warp i does query head i of every group.
   const int c0 = lane * 4;
+  int open_pair[2] = {-1, -1};  // begun before this CTA; going on behind it
   for (int first = 0; first < 2 * kWarps;) {
     const int pair = (first & 1) ? sm.pair_tail[first >> 1] : sm.pair_head[first >> 1];
     int next_part = first + 1;
@@ -507,60 +572,93 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
           }
         }
       }
-      if ((first & 1) && ends) {
-        // nothing left to join
-      } else {  // at most one group begun before this CTA and one that goes on behind it
-        __threadfence();
-        __syncthreads();
-        const int row = pair / H, h = pair - row * H;
-        const int t0 = p.tile_start[row], nt = p.tile_start[row + 1] - t0;
-        const int64_t beg = (int64_t)t0 * H + (int64_t)h * nt;
-        // tile x belongs to CTA ((x + 1) ctas - 1) / total
-        const int from = (int)(((beg + 1) * ctas - 1) / total), to = (int)(((beg + nt) * ctas - 1) / total);
-        const int n = to - from + 1;
-        if (threadIdx.x == 0) sm.last[first & 1] = atomicAdd(&p.tickets[pair], 1u) == (uint32_t)(n - 1);
-        __syncthreads();
-        if (sm.last[first & 1]) {
-          __threadfence();
-          if (warp < r) {
-            auto part_of = [&](int c) { return p.parts + ((int64_t)c * 2 + (c == from ? 1 : 0)) * kPartFloats; };
-            float M = -INFINITY, L = 0.0f;
-            for (int c = from + lane; c <= to; c += 32) M = fmaxf(M, __ldcg(part_of(c) + kRows * kPagedDim + warp));
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = from; c <= to; ++c) {
-              const float* part = part_of(c);
-              const float mi = __ldcg(part + kRows * kPagedDim + warp);
-              const float w = mi == -INFINITY ? 0.0f : exp2_fast(mi - M);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(part + warp * kPagedDim + c0));
-              L = fmaf(w, __ldcg(part + kRows * kPagedDim + kRows + warp), L);
-              acc.x = fmaf(w, v.x, acc.x);
-              acc.y = fmaf(w, v.y, acc.y);
-              acc.z = fmaf(w, v.z, acc.z);
-              acc.w = fmaf(w, v.w, acc.w);
-            }
-            const float inv = 1.0f / L;
-            uint2 y;
-            y.x = BF16 ? pack_bf162(acc.x * inv, acc.y * inv) : pack_half2(acc.x * inv, acc.y * inv);
-            y.y = BF16 ? pack_bf162(acc.z * inv, acc.w * inv) : pack_half2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(p.out + ((int64_t)pair * r + warp) * kPagedDim + c0) = y;
-          }
-          if (threadIdx.x == 0) p.tickets[pair] = 0u;  // ready for the next call
-        }
-      }
+      if (!(first & 1)) open_pair[0] = pair;
+      else if (!ends) open_pair[1] = pair;
     }
     first = pair >= 0 ? next_part : first + 1;
+  }
+  if (open_pair[0] < 0 && open_pair[1] < 0) return;
+
+  // At most one pair was begun before this CTA and one goes on behind it. The last CTA of a
+  // pair to arrive joins its parts.
+  __syncthreads();
+  int from[2], to[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    from[k] = to[k] = 0;
+    if (open_pair[k] < 0) continue;
+    const int row = open_pair[k] / H, h = open_pair[k] - row * H;
+    const int t0 = p.tile_start[row], nt = p.tile_start[row + 1] - t0;
+    const int64_t beg = (int64_t)t0 * H + (int64_t)h * nt;
+    // tile x belongs to CTA ((x + 1) ctas - 1) / total
+    from[k] = (int)(((beg + 1) * ctas - 1) / total);
+    to[k] = (int)(((beg + nt) * ctas - 1) / total);
+    if (threadIdx.x == k * 32)
+      sm.last[k] = take_ticket(&p.tickets[open_pair[k]]) == (uint32_t)(to[k] - from[k]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (open_pair[k] < 0 || !sm.last[k]) continue;
+    if (warp < r) {
+      auto part_of = [&](int c) { return p.parts + ((int64_t)c * 2 + (c == from[k] ? 1 : 0)) * kPartFloats; };
+      float M = -INFINITY, L = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c1 = from[k]; c1 <= to[k]; c1 += 16) {  // 16 parts in flight at a time
+        float mi[16], li[16];
+        float4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float* part = part_of(min(c1 + i, to[k]));
+          mi[i] = c1 + i <= to[k] ? __ldcg(part + kRows * kPagedDim + warp) : -INFINITY;
+          li[i] = __ldcg(part + kRows * kPagedDim + kRows + warp);
+          v[i] = __ldcg(reinterpret_cast<const float4*>(part + warp * kPagedDim + c0));
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mn = fmaxf(mn, mi[i]);
+        const float a = M == -INFINITY ? 0.0f : exp2_fast(M - mn);
+        M = mn;
+        L *= a;
+        acc.x *= a;
+        acc.y *= a;
+        acc.z *= a;
+        acc.w *= a;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float w = mi[i] == -INFINITY ? 0.0f : exp2_fast(mi[i] - M);
+          L = fmaf(w, li[i], L);
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
+        }
+      }
+      const float inv = 1.0f / L;
+      uint2 y;
+      y.x = BF16 ? pack_bf162(acc.x * inv, acc.y * inv) : pack_half2(acc.x * inv, acc.y * inv);
+      y.y = BF16 ? pack_bf162(acc.z * inv, acc.w * inv) : pack_half2(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(p.out + ((int64_t)open_pair[k] * r + warp) * kPagedDim + c0) = y;
+    }
+    if (threadIdx.x == 0) p.tickets[open_pair[k]] = 0u;  // ready for the next call
   }
 }
 
 template <int FMT, bool BF16>
-cudaError_t launch(const PagedDecodeParams& p, int ctas, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<FMT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(Smem));
+cudaError_t launch(const PagedDecodeParams& p, cudaStream_t stream) {
+  static std::atomic<int> sm_count[64];  // per device; set once its kernel may use the shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_decode_kernel<FMT, BF16>, dim3(ctas), dim3(kWarps * 32), sizeof(Smem), stream, p);
+  int sms = dev < 64 ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(paged_decode_kernel<FMT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) sm_count[dev].store(sms, std::memory_order_relaxed);
+  }
+  return launch_pdl(paged_decode_kernel<FMT, BF16>, dim3(std::min(sms, kMaxCtas)), dim3(kWarps * 32), sizeof(Smem), stream, p);
 }
 
 }  // namespace
@@ -571,14 +669,9 @@ size_t paged_workspace_bytes(const PagedGeometry& g) {
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, int fmt, int dtype, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int ctas = std::min(sms, kMaxCtas);
   if (fmt == KVQ_PAGED_INT8)
-    return dtype == KVQ_BF16 ? launch<KVQ_PAGED_INT8, true>(p, ctas, stream) : launch<KVQ_PAGED_INT8, false>(p, ctas, stream);
-  return dtype == KVQ_BF16 ? launch<KVQ_PAGED_E4M3, true>(p, ctas, stream) : launch<KVQ_PAGED_E4M3, false>(p, ctas, stream);
+    return dtype == KVQ_BF16 ? launch<KVQ_PAGED_INT8, true>(p, stream) : launch<KVQ_PAGED_INT8, false>(p, stream);
+  return dtype == KVQ_BF16 ? launch<KVQ_PAGED_E4M3, true>(p, stream) : launch<KVQ_PAGED_E4M3, false>(p, stream);
 }
 
 }  // namespace kvq

@@ -107,6 +107,8 @@ _lock = threading.Lock()
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libkvq.so; raises if it is missing (build it with bit_kv_cache_09_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -12,6 +12,8 @@ on one stream or by events.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import kvq
@@ -27,17 +29,21 @@ def _code(dtype) -> int:
 
 def _rows(name: str, x: torch.Tensor, device, dtype, heads: int, d_head: int) -> int:
     """Checks [rows][heads][d_head] rows (heads contiguous inside a row); returns the row stride in elements."""
+    shape, stride = x.shape, x.stride()
+    if (x.device == device and x.dtype == dtype and len(shape) == 3 and shape[1] == heads and shape[2] == d_head
+            and stride[2] == 1 and (heads == 1 or stride[1] == d_head)):
+        if shape[0] <= 1:
+            return heads * d_head
+        if stride[0] % 8 == 0:
+            return stride[0]
+        raise ValueError(f"{name}: the row stride must be a multiple of 8 elements, not {stride[0]}")
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, expected {device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {x.dtype}")
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d_head:
-        raise ValueError(f"{name} must be [rows][{heads}][{d_head}], not {tuple(x.shape)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d_head):
-        raise ValueError(f"{name}: the heads of a row must lie behind one another (strides {x.stride()})")
-    if x.shape[0] > 1 and x.stride(0) % 8:
-        raise ValueError(f"{name}: the row stride must be a multiple of 8 elements, not {x.stride(0)}")
-    return x.stride(0) if x.shape[0] > 1 else heads * d_head
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d_head:
+        raise ValueError(f"{name} must be [rows][{heads}][{d_head}], not {tuple(shape)}")
+    raise ValueError(f"{name}: the heads of a row must lie behind one another (strides {stride})")
 
 
 def _ints(name: str, x: torch.Tensor, device, n=None) -> int:
@@ -46,6 +52,16 @@ def _ints(name: str, x: torch.Tensor, device, n=None) -> int:
     if n is not None and x.numel() != n:
         raise ValueError(f"{name} must have {n} entries, not {x.numel()}")
     return x.data_ptr()
+
+
+def _launch(device, name: str, *args) -> None:
+    """Calls entry point `name` with `args` and the current stream of `device`, that device being current."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(device, name, *args)
+    status = getattr(kvq.load(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        raise kvq.KVQError(name, status, kvq.kvq_status_string(status))
 
 
 class StepTables:
@@ -96,17 +112,21 @@ class PagedKVCache:
             self.tables = StepTables(self.cfg, self.device)
             self.ws = torch.zeros(max(kvq.kvq_paged_workspace_size(self.cfg), 256), dtype=torch.uint8,
                                   device=self.device)
+        # the arguments that never change
+        self._cfg, self._bufs, self._state, self._step = (ctypes.byref(x) for x in (self.cfg, self.bufs, self.state,
+                                                                                    self.tables.ptrs))
+        self._table, self._ws = self.block_table.data_ptr(), self.ws.data_ptr()
 
-    def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+    def _call(self, name: str, *args) -> None:
+        """lib.name(*args, stream) with the cache's device current."""
+        _launch(self.device, name, *args)
 
     def step(self, new_tokens: torch.Tensor, commit: bool = True) -> StepTables:
         """Builds the tables of a step that adds new_tokens[i] tokens to request i (int32
         [n_requests] on the device; -1 releases the request). With commit=False lens and
         free_count stay as they were, so the step can be built again."""
         ptr = _ints("new_tokens", new_tokens, self.device, self.cfg.n_requests)
-        with torch.cuda.device(self.device):
-            kvq.kvq_paged_step_tables(self.cfg, self.state, ptr, self.tables.ptrs, int(commit), self._stream())
+        self._call("kvq_paged_step_tables", self._cfg, self._state, ptr, self._step, int(commit))
         return self.tables
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -117,20 +137,17 @@ class PagedKVCache:
         vs = _rows("v", v, self.device, self.dtype, c.n_kv_heads, c.d_head)
         if k.shape[0] != v.shape[0]:
             raise ValueError(f"k has {k.shape[0]} rows, v {v.shape[0]}")
-        with torch.cuda.device(self.device):
-            kvq.kvq_paged_append(c, self.bufs, self.block_table.data_ptr(), self.tables.ptrs, layer, k.shape[0],
-                                 k.data_ptr(), ks, v.data_ptr(), vs, self._stream())
+        self._call("kvq_paged_append", self._cfg, self._bufs, self._table, self._step, layer, k.shape[0], k.data_ptr(), ks,
+                   v.data_ptr(), vs)
 
     def dequantize(self, layer: int, slots: torch.Tensor):
         """Keys and values kept at `slots` (int32, as in StepTables.slots): two float32
         [len(slots)][n_kv_heads][d_head] tensors."""
         c = self.cfg
-        ptr = _ints("slots", slots, self.device)
-        with torch.cuda.device(self.device):
-            k = torch.empty((slots.numel(), c.n_kv_heads, c.d_head), dtype=torch.float32, device=self.device)
-            v = torch.empty_like(k)
-            kvq.kvq_paged_dequantize(c, self.bufs, layer, slots.numel(), ptr, k.data_ptr(), v.data_ptr(),
-                                     self._stream())
+        ptr, n = _ints("slots", slots, self.device), slots.numel()
+        k = torch.empty((n, c.n_kv_heads, c.d_head), dtype=torch.float32, device=self.device)
+        v = torch.empty_like(k)
+        self._call("kvq_paged_dequantize", self._cfg, self._bufs, layer, n, ptr, k.data_ptr(), v.data_ptr())
         return k, v
 
     def attention(self, layer: int, q: torch.Tensor, softmax_scale: float, out: torch.Tensor = None) -> torch.Tensor:
@@ -141,15 +158,13 @@ class PagedKVCache:
         qs = _rows("q", q, self.device, self.dtype, self.n_q, c.d_head)
         if q.shape[0] != c.n_requests:
             raise ValueError(f"q must have {c.n_requests} rows, not {q.shape[0]}")
-        with torch.cuda.device(self.device):
-            fresh = out is None
-            if fresh:
-                out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-            elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
-                raise ValueError(f"out must be a contiguous {self.dtype} tensor of shape {tuple(q.shape)} on {self.device}")
-            kvq.kvq_paged_decode_attention(c, self.bufs, self.block_table.data_ptr(), self.tables.ptrs, layer,
-                                           q.data_ptr(), qs, softmax_scale, out.data_ptr(), int(fresh),
-                                           self.ws.data_ptr(), self.ws.numel(), self._stream())
+        fresh = out is None
+        if fresh:
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {self.dtype} tensor of shape {tuple(q.shape)} on {self.device}")
+        self._call("kvq_paged_decode_attention", self._cfg, self._bufs, self._table, self._step, layer, q.data_ptr(), qs,
+                   softmax_scale, out.data_ptr(), fresh, self._ws, self.ws.numel())
         return out
 
     def check_errors(self) -> None:
@@ -159,7 +174,7 @@ class PagedKVCache:
             bits = int(self.tables.status[0].item())
             if bits:
                 self.tables.status[0].zero_()
-            word = kvq.kvq_decode_error(self.ws.data_ptr(), self.ws.numel(), self._stream())
+            word = kvq.kvq_decode_error(self._ws, self.ws.numel(), torch.cuda.current_stream().cuda_stream)
         if bits:
             raise kvq.KVQStepError(bits)
         if word:

@@ -7,10 +7,12 @@ tokens from the 16-bit rows before they are quantized.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import kvq
-from .paged import _code, _ints, _rows
+from .paged import _code, _ints, _launch, _rows
 
 
 class PromptAttention:
@@ -47,20 +49,18 @@ class PromptAttention:
         if q_start.numel() < 2:
             raise ValueError("q_start needs one entry per sequence and one for the end")
         kp = qp if kv_start is None else _ints("kv_start", kv_start, self.device, q_start.numel())
-        with torch.cuda.device(self.device):
-            fresh = out is None
-            if fresh:
-                out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-            elif out.shape != q.shape:
-                raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
-            os = _rows("out", out, self.device, self.dtype, self.n_q, self.d_head)
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if return_lse else None
-            args = kvq.kvq_prompt_args(self.n_kv, self.gqa, self.d_head, self._dtype_code, q_start.numel() - 1,
-                                       int(causal), int(fresh or return_lse), q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                       qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
-                                       lse.data_ptr() if return_lse else None)
-            kvq.kvq_prompt_attention(args, self.ws.data_ptr(), self.ws.numel(),
-                                     torch.cuda.current_stream(self.device).cuda_stream)
+        fresh = out is None
+        if fresh:
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        elif out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}, not {tuple(out.shape)}")
+        os = _rows("out", out, self.device, self.dtype, self.n_q, self.d_head)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if return_lse else None
+        args = kvq.kvq_prompt_args(self.n_kv, self.gqa, self.d_head, self._dtype_code, q_start.numel() - 1, causal,
+                                   fresh or return_lse, q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
+                                   lse.data_ptr() if return_lse else None)
+        _launch(self.device, "kvq_prompt_attention", ctypes.byref(args), self.ws.data_ptr(), 256)
         return (out, lse) if return_lse else out
 
     def check_errors(self) -> None:
