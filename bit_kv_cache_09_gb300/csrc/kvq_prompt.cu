@@ -1,11 +1,25 @@
-// kvq_prompt.cu — attention of packed prompts.
+// kvq_prompt.cu — attention of packed prompts on the 5th-generation tensor cores.
 //
-// One warp per (query row, query head): lanes score 32 keys at a time, a running maximum
-// and sum carries the softmax, and each lane accumulates 4 channels of the values.
+//   s_ij = scale q_i . k_j,  m_i = max_j s_ij,  o_i = sum_j 2^(s_ij - m_i) v_j / sum_j 2^(s_ij - m_i)
+// in one pass over the keys with a running maximum and sum per row.
+//
+// Bound by the tensor cores: 4 * 128 operations per (query row, key). A CTA holds two tiles
+// of 128 query rows. A tile is 128 / r tokens of all r query heads of one kv head (the rows of
+// a token lie behind one another), so a key tile serves every head of its group. Keys and values
+// come in tiles of 128 tokens through a ring of 5 stages filled by TMA. Per key tile j and
+// query tile t the MMA warp issues O_t += P_t(j) V_j and S_t(j+1) = Q_t K_{j+1}^T; while
+// one tile's four softmax warps turn S into P, the tensor cores work for the other tile.
+// S (binary32) and P (16 bits, over the columns of S) and O live in tensor memory:
+//   columns 0..127 S_0 / P_0, 128..255 S_1 / P_1, 256..383 O_0, 384..511 O_1.
+// A softmax thread owns one row, so maxima and sums need no exchange. The running maximum
+// only moves (and O is only rescaled) when a row's maximum grew by more than 2^8: weights
+// stay below 2^15, within binary16.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_kernels.h"
 #include "kvq_prompt.h"
@@ -13,100 +27,509 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 8, kDim = 128;
+constexpr int kDim = 128;
+constexpr int kTile = 128;                    // query rows of a tile, keys of a tile
+constexpr int kPanel = kTile * 128;           // bytes: 128 rows of 64 channels, 128-byte swizzle
+constexpr int kTileBytes2 = 2 * kPanel;       // a 128 x 128 tile: two panels
+constexpr int kStages = 5;
+constexpr int kThreads = 320;                 // 2 x 4 softmax warps, MMA warp, TMA warp
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr float kMoveAt = 8.0f;               // the maximum moves when it grew by 2^8
+// Weights are held times 2^7: with the above below 2^15, and binary16 resolves 2^-31 of the
+// largest weight, so that a long flat tail of the softmax is not lost.
+constexpr float kWeightExp = 7.0f;
 
+struct Smem {
+  uint8_t q[2][kTileBytes2];
+  uint8_t kv[kStages][kTileBytes2];
+  uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_ready[2], o_full[2], done;
+  uint32_t tmem;
+  int seq, tile, abort;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred q;\nmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Waits for a phase, at most wait_ns or until another warp gave up. The first to give up says so
+// in the error word and to the CTA; every role then leaves its loop.
+__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint64_t wait_ns, volatile int* abort, uint32_t* err) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    if (bar_try(b, parity)) return true;
+    if (*abort) return false;
+    if (now_ns() - t0 > wait_ns) {
+      *abort = 1;
+      atomicOr(err, KVQ_DECODE_ERR_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, const PromptParams& p, Smem& sm) {
+  for (int i = 0; i < 32; ++i)
+    if (bar_try(b, parity)) return true;
+  return bar_wait_slow(b, parity, p.wait_ns, &sm.abort, p.err);
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c, int head, int token, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(c), "r"(head), "r"(token), "r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle. A tile is two panels of 64 channels;
+// groups of 8 rows are 1024 bytes apart.
+constexpr uint64_t kDescBase = (uint64_t(2) << 61) | (uint64_t(1) << 46) | (uint64_t(1024 >> 4) << 32);
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {  // rows x channels: the product runs along a row
+  return kDescBase | (uint64_t(1) << 16) | (addr >> 4);
+}
+__device__ __forceinline__ uint64_t desc_cols(uint32_t addr) {  // the product runs over the rows; panels side by side
+  return kDescBase | (uint64_t(kPanel >> 4) << 16) | (addr >> 4);
+}
+// Instruction descriptor: binary32 accumulator, 16-bit operands, 128 x 128.
 template <bool BF16>
-__device__ __forceinline__ float2 pair(uint32_t w) {
-  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+__device__ constexpr uint32_t idesc(bool b_cols) {
+  return (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_cols ? 1u << 16 : 0u) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               ::"r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               ::"r"(d), "r"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {  // arrives when every MMA issued so far is done
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define KVQ_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+#define KVQ_R16(x, i) KVQ_R4(x, i), KVQ_R4(x, i + 4), KVQ_R4(x, i + 8), KVQ_R4(x, i + 12)
+#define KVQ_W4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
+#define KVQ_W16(x, i) KVQ_W4(x, i), KVQ_W4(x, i + 4), KVQ_W4(x, i + 8), KVQ_W4(x, i + 12)
+// 32 columns of this warp's 32 lanes (rows).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KVQ_R16(x, 0), KVQ_R16(x, 16) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(addr), KVQ_W16(x, 0), KVQ_W16(x, 16) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A sequence's rows, kept inside the arrays whatever the starts say.
+struct Span {
+  int q0, lq, k0, lk;
+};
+__device__ __forceinline__ Span span_of(const PromptParams& p, int s) {
+  Span x;
+  x.q0 = min(max(p.q_start[s], 0), p.n_q);
+  x.lq = min(max(p.q_start[s + 1], x.q0), p.n_q) - x.q0;
+  x.k0 = min(max(p.kv_start[s], 0), p.n_kv);
+  x.lk = min(max(p.kv_start[s + 1], x.k0), p.n_kv) - x.k0;
+  return x;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) prompt_kernel(const PromptParams p) {
-  __shared__ float q_s[kWarps][kDim];
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tokens = kTile / p.r;  // of a query tile
+  const int h = blockIdx.x % p.H;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.q_full[i], 1);
+      bar_init(&sm.s_full[i], 1);
+      bar_init(&sm.p_ready[i], kTile);
+      bar_init(&sm.o_full[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(&sm.kv_full[i], 1);
+      bar_init(&sm.kv_empty[i], 1);
+    }
+    bar_init(&sm.done, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   pdl_wait();
   pdl_allow_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, nq = p.H * p.r;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
-  const int row = (int)(item / nq), head = (int)(item % nq), h = head / p.r;
-  if (row >= p.n_q) return;
-  int lo = 0, hi = p.n_seqs;  // last sequence that starts at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.q_start[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int q0 = max(p.q_start[lo], 0), q1 = min(p.q_start[lo + 1], p.n_q);
-  if (row < q0 || row >= q1) {
-    if (p.zero_rest) *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kDim + lane * 4) = make_uint2(0u, 0u);
-    if (p.zero_rest && p.lse && lane == 0) p.lse[(int64_t)row * nq + head] = -INFINITY;
-    return;
-  }
-  const int k0 = min(max(p.kv_start[lo], 0), p.n_kv), k1 = min(max(p.kv_start[lo + 1], k0), p.n_kv);
-  const int see = p.causal ? max(0, min(k1 - k0, row - q0 + 1 + (k1 - k0) - (q1 - q0))) : k1 - k0;
-  for (int c = lane; c < kDim / 2; c += 32) {
-    const float2 f = pair<BF16>(*reinterpret_cast<const uint32_t*>(p.q + row * p.q_stride + head * kDim + 2 * c));
-    q_s[warp][2 * c] = f.x;
-    q_s[warp][2 * c + 1] = f.y;
-  }
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < see; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    if (j < see) {
-      const uint4* kr = reinterpret_cast<const uint4*>(p.k + (k0 + j) * p.k_stride + h * kDim);
-      s = 0.0f;
-      for (int c = 0; c < kDim / 8; ++c) {
-        const uint4 x = kr[c];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if (warp == 0) {  // which sequence, and which of its pairs of tiles (the longest rows first)
+    int want = blockIdx.x / p.H, seq = -1, tile = 0;
+    for (int s0 = 0; s0 < p.n_seqs && seq < 0; s0 += 32) {
+      const int s = s0 + lane;
+      const int n = s < p.n_seqs ? (span_of(p, s).lq + 2 * tokens - 1) / (2 * tokens) : 0;
+      int sum = n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = pair<BF16>(w[i]);
-          s = fmaf(f.x, q_s[warp][c * 8 + i * 2], s);
-          s = fmaf(f.y, q_s[warp][c * 8 + i * 2 + 1], s);
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, sum > want);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        seq = s0 + l;
+        tile = __shfl_sync(0xffffffffu, sum - 1, l) - want;
+      } else {
+        want -= __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
+    if (lane == 0) {
+      sm.seq = seq;
+      sm.tile = tile;
+    }
+  }
+  if (p.zero_rest) {  // rows of no sequence, shared out over the CTAs
+    const int first = min(max(p.q_start[0], 0), p.n_q), last = min(max(p.q_start[p.n_seqs], 0), p.n_q);
+    const int nq = p.H * p.r;
+    for (int64_t i = blockIdx.x; i < (int64_t)first + (p.n_q - last); i += gridDim.x) {
+      const int64_t row = i < first ? i : last + (i - first);
+      for (int c = threadIdx.x; c < nq * (kDim / 8); c += kThreads)
+        *reinterpret_cast<uint4*>(p.out + row * p.out_stride + c * 8) = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = threadIdx.x; p.lse && c < nq; c += kThreads) p.lse[row * nq + c] = -INFINITY;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int seq = sm.seq;
+  if (seq >= 0) {
+    const Span sp = span_of(p, seq);
+    const int t0 = sm.tile * 2 * tokens;  // first token, within the sequence
+    const int shift = sp.lk - sp.lq;      // causal: token i sees keys 0 .. i + shift
+    int n_keys[2], n[2];                  // keys that some row of the tile sees, key tiles
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int beg = t0 + t * tokens, end = min(sp.lq, beg + tokens);
+      n_keys[t] = beg >= sp.lq ? 0 : p.causal ? min(max(end + shift, 0), sp.lk) : sp.lk;
+      n[t] = (n_keys[t] + kTile - 1) / kTile;
+    }
+    const int n_max = max(n[0], n[1]);
+
+    if (warp == kTmaWarp) {
+      if (lane == 0 && n_max > 0) {
+        int c = 0, landed = 0;  // key and value tiles sent for; of them, waited for here (after giving up)
+        bool ok = true;
+        auto load_kv = [&](const CUtensorMap* map, int j) {
+          const int s = c % kStages;
+          if (c >= kStages) ok = bar_wait(&sm.kv_empty[s], (c / kStages - 1) & 1, p, sm);
+          if (!ok) return;
+          bar_expect(&sm.kv_full[s], kTileBytes2);
+          tma_load(sm.kv[s], map, 0, h, sp.k0 + j * kTile, &sm.kv_full[s]);
+          tma_load(sm.kv[s] + kPanel, map, 64, h, sp.k0 + j * kTile, &sm.kv_full[s]);
+          ++c;
+        };
+        auto load_q = [&](int t) {
+          if (n[t] == 0) return;
+          bar_expect(&sm.q_full[t], 2 * tokens * p.r * 128);
+          tma_load(sm.q[t], &q_map, 0, h * p.r, sp.q0 + t0 + t * tokens, &sm.q_full[t]);
+          tma_load(sm.q[t] + kPanel, &q_map, 64, h * p.r, sp.q0 + t0 + t * tokens, &sm.q_full[t]);
+        };
+        load_q(0);
+        load_kv(&k_map, 0);
+        load_q(1);
+        load_kv(&v_map, 0);
+        for (int j = 1; j < n_max && ok; ++j) {
+          load_kv(&k_map, j);
+          if (ok) load_kv(&v_map, j);
+        }
+        if (!ok) {  // let what is in flight land before the CTA may end
+          for (int t = 0; t < 2; ++t)
+            if (n[t] > 0) bar_wait_slow(&sm.q_full[t], 0, p.wait_ns, &landed, p.err);
+          for (int i = max(0, c - kStages); i < c; ++i)
+            bar_wait_slow(&sm.kv_full[i % kStages], (i / kStages) & 1, p.wait_ns, &landed, p.err);
         }
       }
-      s *= p.scale_log2;
-    }
-    float mn = s;
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      bool ok = true;
+      const uint32_t q_addr[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])};
+      auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
+        if (lane == 0) {
+          const uint32_t k_addr = smem_u32(sm.kv[stage]);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-    mn = fmaxf(m, mn);
-    const float a = exp2f(m - mn), e = j < see ? exp2f(s - mn) : 0.0f;
-    m = mn;
-    float sum = e;
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t off = (s >> 2) * kPanel + (s & 3) * 32;
+            mma_ss(tmem + t * kTile, desc_rows(q_addr[t] + off), desc_rows(k_addr + off), idesc<BF16>(false), s > 0);
+          }
+          mma_commit(&sm.s_full[t]);
+        }
+        __syncwarp();
+      };
+      if (n_max > 0) {
+        ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[0], 0, p, sm));
+        for (int t = 0; t < 2 && ok; ++t)
+          if (n[t] > 0) {
+            ok = __all_sync(0xffffffffu, bar_wait(&sm.q_full[t], 0, p, sm));
+            if (ok) scores(t, 0);
+          }
+        if (lane == 0 && ok) mma_commit(&sm.kv_empty[0]);
+      }
+      for (int j = 0; j < n_max && ok; ++j) {
+        const int cv = 2 * j + 1, ck = 2 * j + 2, sv = cv % kStages, sk = ck % kStages;
+        ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[sv], (cv / kStages) & 1, p, sm));
+        if (!ok) break;
+        // Rows behind the sequence's last key belong to another sequence. Weights are 0 there,
+        // but 0 times an infinity is not: the product stops at the last 16 rows that hold a
+        // key, and what follows the last key among those is cleared.
+        const int rest = sp.lk - j * kTile;
+        if (rest < kTile && (rest & 15)) {
+          for (int i = lane; i < (16 - (rest & 15)) * 16; i += 32) {
+            const int row = rest + (i >> 4), c = i & 15;
+            *reinterpret_cast<uint4*>(sm.kv[sv] + (c >> 3) * kPanel + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        const uint32_t v_addr = smem_u32(sm.kv[sv]);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j < n[t]) {
+            ok = __all_sync(0xffffffffu, bar_wait(&sm.p_ready[t], j & 1, p, sm));
+            if (!ok) break;
+            fence_after();
+            if (lane == 0) {
+              const int steps = min(8, (n_keys[t] - j * kTile + 15) / 16);
+              for (int s = 0; s < steps; ++s)
+                mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + s * 8, desc_cols(v_addr + s * 2048), idesc<BF16>(true),
+                       j > 0 || s > 0);
+              if (j == n[t] - 1) mma_commit(&sm.o_full[t]);
+            }
+            __syncwarp();
+          }
+          if (j + 1 < n[t]) {
+            ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm));
+            if (ok) scores(t, sk);
+          }
+        }
+        if (lane == 0 && ok) {
+          mma_commit(&sm.kv_empty[sv]);
+          if (j + 1 < n_max) mma_commit(&sm.kv_empty[sk]);
+        }
+      }
+      // nothing of this CTA is in flight when it ends
+      if (lane == 0 && n_max > 0) {
+        int over = 0;
+        mma_commit(&sm.done);
+        bar_wait_slow(&sm.done, 0, p.wait_ns, &over, p.err);
+      }
+      __syncwarp();
+    } else {
+      const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_addr = tmem + lanes + t * kTile, o_addr = tmem + lanes + 256 + t * kTile;
+      const int token = t0 + t * tokens + row / p.r, head = h * p.r + row % p.r;
+      const bool mine = row < tokens * p.r && token < sp.lq;
+      // keys this row sees (rows of no token: as many as the tile, nothing to mask)
+      const int see = !mine ? n[t] * kTile : p.causal ? min(max(token + 1 + shift, 0), sp.lk) : sp.lk;
+      const float scale = p.scale_log2;
+      float m = -INFINITY, l = 0.0f;  // m: maximum in use, of scale * s
+      bool ok = true;
+      for (int j = 0; j < n[t]; ++j) {
+        ok = __all_sync(0xffffffffu, bar_wait(&sm.s_full[t], j & 1, p, sm));
+        if (!ok) break;
+        fence_after();
+        uint32_t x[kTile];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * a + sum;
-    for (int c = 0; c < 4; ++c) o[c] *= a;
-    const int n = min(32, see - j0);
-    for (int t = 0; t < n; ++t) {
-      const float w = __shfl_sync(0xffffffffu, e, t);
-      const uint2 x = *reinterpret_cast<const uint2*>(p.v + (k0 + j0 + t) * p.v_stride + h * kDim + lane * 4);
-      const float2 f0 = pair<BF16>(x.x), f1 = pair<BF16>(x.y);
-      o[0] = fmaf(w, f0.x, o[0]);
-      o[1] = fmaf(w, f0.y, o[1]);
-      o[2] = fmaf(w, f1.x, o[2]);
-      o[3] = fmaf(w, f1.y, o[3]);
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, x + c);
+        tmem_wait_ld();
+        const int left = see - j * kTile;  // visible keys of this tile
+        if (__any_sync(0xffffffffu, left < kTile) || scale == 0.0f) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) {
+            const float s = scale == 0.0f ? 0.0f : __uint_as_float(x[c]);
+            x[c] = __float_as_uint(c < left ? s : -INFINITY);
+          }
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(x[c]);
+#pragma unroll
+        for (int c = 4; c < kTile; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+        const float scale_use = scale == 0.0f ? 1.0f : scale;
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_use;
+        const bool move = mt > m + kMoveAt || m == -INFINITY;
+        const float m_old = m;
+        if (move) m = fmaxf(m, mt);
+        if (j > 0 && __any_sync(0xffffffffu, move && m_old != -INFINITY)) {
+          // every MMA issued before S_t(j) is done, so O_t stands still
+          const float a = exp2_fast(m_old - (m == -INFINITY ? 0.0f : m));
+          const float f = m_old == -INFINITY || !move ? 1.0f : a;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < kDim; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(o_addr + c, o);
+          }
+        }
+        const float off = kWeightExp - (m == -INFINITY ? 0.0f : m);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), scale_use, off));
+            const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), scale_use, off));
+            sum[c & 2] += a;
+            sum[(c & 2) + 1] += b;
+            w[c / 2] = pack2<BF16>(a, b);
+          }
+          tmem_st32(s_addr + c0 / 2, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        fence_before();
+        bar_arrive(&sm.p_ready[t]);
+      }
+      if (n[t] > 0 && ok) {
+        ok = __all_sync(0xffffffffu, bar_wait(&sm.o_full[t], 0, p, sm));
+        fence_after();
+      }
+      if (ok && t0 + t * tokens < sp.lq) {
+        const float inv = see > 0 ? 1.0f / l : 0.0f;
+        const int64_t at = sp.q0 + token;
+#pragma unroll
+        for (int c = 0; c < kDim; c += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          if (n[t] > 0) {
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+          }
+          if (mine) {
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              y[i] = see > 0 ? pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+            uint4* out = reinterpret_cast<uint4*>(p.out + at * p.out_stride + head * kDim + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+        }
+        if (p.lse && mine)
+          p.lse[at * (p.H * p.r) + head] = see > 0 ? (m - kWeightExp + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
     }
   }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  for (int c = 0; c < 4; ++c) {
-    const float y = see > 0 ? o[c] * inv : 0.0f;
-    p.out[row * p.out_stride + head * kDim + lane * 4 + c] =
-        BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
   }
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)row * nq + head] = see > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// Rows [tokens][heads][128] of 16 bits; boxes of 64 channels x box_heads x box_tokens.
+bool make_map(EncodeFn fn, CUtensorMap* map, const void* p, int heads, int64_t rows, int64_t stride, int box_heads,
+              int box_tokens, int dtype) {
+  *map = CUtensorMap{};
+  if (rows == 0) return true;  // never used
+  const cuuint64_t dims[3] = {kDim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {kDim * 2, (cuuint64_t)(rows > 1 ? stride : (int64_t)heads * kDim) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, ones[3] = {1, 1, 1};
+  return fn(map, dtype == KVQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16>
+cudaError_t launch(const PromptParams& p, int64_t ctas, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(Smem) + 1024;
+  static std::atomic<bool> ready[64];  // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(prompt_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  return launch_pdl(prompt_kernel<BF16>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, q, k, v);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const PromptParams& p, int dtype, cudaStream_t stream) {
-  const int64_t items = (int64_t)p.n_q * p.H * p.r;
-  const dim3 grid((unsigned)((items + kWarps - 1) / kWarps));
-  return dtype == KVQ_BF16 ? launch_pdl(prompt_kernel<true>, grid, dim3(kWarps * 32), 0, stream, p)
-                           : launch_pdl(prompt_kernel<false>, grid, dim3(kWarps * 32), 0, stream, p);
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const int tokens = kTile / p.r;
+  CUtensorMap q, k, v;
+  if (!make_map(fn, &q, p.q, p.H * p.r, p.n_q, p.q_stride, p.r, tokens, dtype) ||
+      !make_map(fn, &k, p.k, p.H, p.n_kv, p.k_stride, 1, kTile, dtype) ||
+      !make_map(fn, &v, p.v, p.H, p.n_kv, p.v_stride, 1, kTile, dtype))
+    return cudaErrorInvalidValue;
+  // pairs of tiles: one per 2 * tokens tokens of a sequence, at least one for a sequence with a token
+  const int64_t ctas = (p.n_q / (2 * tokens) + std::min(p.n_q, p.n_seqs)) * (int64_t)p.H;
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  return dtype == KVQ_BF16 ? launch<true>(p, ctas, q, k, v, stream) : launch<false>(p, ctas, q, k, v, stream);
 }
 
 }  // namespace kvq

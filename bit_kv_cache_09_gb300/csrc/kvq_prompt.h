@@ -16,7 +16,7 @@ struct PromptParams {
   const int32_t *q_start, *kv_start;
   int64_t q_stride, k_stride, v_stride, out_stride;  // elements
   int32_t n_q, n_kv, n_seqs, H, r, causal, zero_rest;
-  float scale_log2;
+  float scale_log2;  // softmax_scale * log2(e)
   uint32_t* err;
   uint64_t wait_ns;
 };
