@@ -32,7 +32,9 @@ constexpr int kTile = 128;                    // query rows of a tile, keys of a
 constexpr int kPanel = kTile * 128;           // bytes: 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes2 = 2 * kPanel;       // a 128 x 128 tile: two panels
 constexpr int kStages = 5;
-constexpr int kThreads = 320;                 // 2 x 4 softmax warps, MMA warp, TMA warp
+constexpr int kThreads = 384;                 // 2 x 4 softmax warps; MMA warp, TMA warp and two that idle
+// Registers of a thread: 168 at launch (384 x 168 = 64512); the softmax warps take 208, the
+// last four give theirs back (8 x 32 x 208 + 4 x 32 x 88 = 64512).
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
 constexpr float kMoveAt = 8.0f;               // the maximum moves when it grew by 2^8
 // Weights are held times 2^7: with the above below 2^15, and binary16 resolves 2^-31 of the
@@ -72,7 +74,7 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 // Waits for a phase, at most wait_ns or until another warp gave up. The first to give up says so
 // in the error word and to the CTA; every role then leaves its loop.
-__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint64_t wait_ns, volatile int* abort, uint32_t* err) {
+__device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint64_t wait_ns, volatile int* abort, uint32_t* err) {
   const uint64_t t0 = now_ns();
   for (;;) {
     if (bar_try(b, parity)) return true;
@@ -88,6 +90,15 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, const Pro
   for (int i = 0; i < 32; ++i)
     if (bar_try(b, parity)) return true;
   return bar_wait_slow(b, parity, p.wait_ns, &sm.abort, p.err);
+}
+
+// One lane of the (converged) warp. Code behind this predicate, and not behind a test of the lane
+// number, issues its MMAs without a loop that makes their operands uniform (75 -> 64 cycles each
+// and less, so that the tensor cores and not the issue set the pace).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+  return is != 0;
 }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c, int head, int token, uint64_t* bar) {
@@ -135,11 +146,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : KVQ_R16(x, 0), KVQ_R16(x, 16) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(addr), KVQ_W16(x, 0), KVQ_W16(x, 16) : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : KVQ_R16(x, 0) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), KVQ_W16(x, 0) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -148,6 +163,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two binary32 lanes in one register pair.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 split(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -255,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int n_max = max(n[0], n[1]);
 
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kTmaWarp) {
-      if (lane == 0 && n_max > 0) {
+      if (elect_one() && n_max > 0) {
         int c = 0, landed = 0;  // key and value tiles sent for; of them, waited for here (after giving up)
         bool ok = true;
         auto load_kv = [&](const CUtensorMap* map, int j) {
@@ -291,78 +333,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
-      bool ok = true;
-      const uint32_t q_addr[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])};
-      auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
-        if (lane == 0) {
-          const uint32_t k_addr = smem_u32(sm.kv[stage]);
+      if (elect_one() && n_max > 0) {
+        bool ok = true;
+        const uint32_t q_addr[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])}, kv_addr = smem_u32(sm.kv[0]);
+        auto scores = [&](int t, int stage) {  // S_t = Q_t K^T
+          const uint64_t a = desc_rows(q_addr[t]), b = desc_rows(kv_addr + stage * kTileBytes2);
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * kPanel + (s & 3) * 32;
-            mma_ss(tmem + t * kTile, desc_rows(q_addr[t] + off), desc_rows(k_addr + off), idesc<BF16>(false), s > 0);
+            const uint32_t off = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
+            mma_ss(tmem + t * kTile, a + off, b + off, idesc<BF16>(false), s > 0);
           }
           mma_commit(&sm.s_full[t]);
-        }
-        __syncwarp();
-      };
-      if (n_max > 0) {
-        ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[0], 0, p, sm));
-        for (int t = 0; t < 2 && ok; ++t)
-          if (n[t] > 0) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm.q_full[t], 0, p, sm));
+        };
+        ok = bar_wait(&sm.kv_full[0], 0, p, sm);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && n[t] > 0) {
+            ok = bar_wait(&sm.q_full[t], 0, p, sm);
             if (ok) scores(t, 0);
           }
-        if (lane == 0 && ok) mma_commit(&sm.kv_empty[0]);
-      }
-      for (int j = 0; j < n_max && ok; ++j) {
-        const int cv = 2 * j + 1, ck = 2 * j + 2, sv = cv % kStages, sk = ck % kStages;
-        ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[sv], (cv / kStages) & 1, p, sm));
-        if (!ok) break;
-        // Rows behind the sequence's last key belong to another sequence. Weights are 0 there,
-        // but 0 times an infinity is not: the product stops at the last 16 rows that hold a
-        // key, and what follows the last key among those is cleared.
-        const int rest = sp.lk - j * kTile;
-        if (rest < kTile && (rest & 15)) {
-          for (int i = lane; i < (16 - (rest & 15)) * 16; i += 32) {
-            const int row = rest + (i >> 4), c = i & 15;
-            *reinterpret_cast<uint4*>(sm.kv[sv] + (c >> 3) * kPanel + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        const uint32_t v_addr = smem_u32(sm.kv[sv]);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j < n[t]) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm.p_ready[t], j & 1, p, sm));
-            if (!ok) break;
-            fence_after();
-            if (lane == 0) {
-              const int steps = min(8, (n_keys[t] - j * kTile + 15) / 16);
-              for (int s = 0; s < steps; ++s)
-                mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + s * 8, desc_cols(v_addr + s * 2048), idesc<BF16>(true),
-                       j > 0 || s > 0);
-              if (j == n[t] - 1) mma_commit(&sm.o_full[t]);
+        if (ok) mma_commit(&sm.kv_empty[0]);
+        for (int j = 0; j < n_max && ok; ++j) {
+          const int cv = 2 * j + 1, ck = 2 * j + 2, sv = cv % kStages, sk = ck % kStages;
+          ok = bar_wait(&sm.kv_full[sv], (cv / kStages) & 1, p, sm);
+          if (!ok) break;
+          // Rows behind the sequence's last key belong to another sequence. Weights are 0 there,
+          // but 0 times an infinity is not: the product stops at the last 16 rows that hold a
+          // key, and what follows the last key among those is cleared.
+          const int rest = sp.lk - j * kTile;
+          if (rest < kTile && (rest & 15)) {
+            for (int i = 0; i < (16 - (rest & 15)) * 16; ++i) {
+              const int row = rest + (i >> 4), c = i & 15;
+              *reinterpret_cast<uint4*>(sm.kv[sv] + (c >> 3) * kPanel + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
-            __syncwarp();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          if (j + 1 < n[t]) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm));
-            if (ok) scores(t, sk);
+          const uint64_t v_desc = desc_cols(kv_addr + sv * kTileBytes2);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && j < n[t]) {
+              ok = bar_wait(&sm.p_ready[t], j & 1, p, sm);
+              if (ok) {
+                fence_after();
+                const int steps = (n_keys[t] - j * kTile + 15) / 16;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  if (s < steps)
+                    mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + s * 8, v_desc + s * (2048 >> 4), idesc<BF16>(true),
+                           j > 0 || s > 0);
+                if (j == n[t] - 1) mma_commit(&sm.o_full[t]);
+              }
+            }
+            if (ok && j + 1 < n[t]) {
+              ok = bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm);
+              if (ok) scores(t, sk);
+            }
+          }
+          if (ok) {
+            mma_commit(&sm.kv_empty[sv]);
+            if (j + 1 < n_max) mma_commit(&sm.kv_empty[sk]);
           }
         }
-        if (lane == 0 && ok) {
-          mma_commit(&sm.kv_empty[sv]);
-          if (j + 1 < n_max) mma_commit(&sm.kv_empty[sk]);
-        }
-      }
-      // nothing of this CTA is in flight when it ends
-      if (lane == 0 && n_max > 0) {
+        // nothing of this CTA is in flight when it ends
         int over = 0;
         mma_commit(&sm.done);
         bar_wait_slow(&sm.done, 0, p.wait_ns, &over, p.err);
       }
       __syncwarp();
-    } else {
+    } else if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
       const int t = warp >> 2, row = (warp & 3) * 32 + lane;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_addr = tmem + lanes + t * kTile, o_addr = tmem + lanes + 256 + t * kTile;
@@ -393,7 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(x[c]);
 #pragma unroll
-        for (int c = 4; c < kTile; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+        for (int c = 4; c < kTile - 4; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(x[c + i]), __uint_as_float(x[c + 4 + i]));
+#pragma unroll
+        for (int c = kTile - 4; c < kTile; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
         const float scale_use = scale == 0.0f ? 1.0f : scale;
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_use;
         const bool move = mt > m + kMoveAt || m == -INFINITY;
@@ -405,31 +448,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = m_old == -INFINITY || !move ? 1.0f : a;
           l *= f;
 #pragma unroll
-          for (int c = 0; c < kDim; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c, o);
+          for (int c = 0; c < kDim; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(o_addr + c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(o_addr + c, o);
           }
         }
         const float off = kWeightExp - (m == -INFINITY ? 0.0f : m);
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint64_t sum[2] = {0ull, 0ull};
+        const uint64_t scale2 = both(scale_use, scale_use), off2 = both(off, off);
 #pragma unroll
-        for (int c0 = 0; c0 < kTile; c0 += 64) {
-          uint32_t w[32];
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), scale_use, off));
-            const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), scale_use, off));
-            sum[c & 2] += a;
-            sum[(c & 2) + 1] += b;
+          for (int c = 0; c < 32; c += 2) {
+            const float2 e = split(fma2(both(__uint_as_float(x[c0 + c]), __uint_as_float(x[c0 + c + 1])), scale2, off2));
+            const float a = exp2_fast(e.x), b = exp2_fast(e.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], both(a, b));
             w[c / 2] = pack2<BF16>(a, b);
           }
-          tmem_st32(s_addr + c0 / 2, w);
+          tmem_st16(s_addr + c0 / 2, w);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 total = split(add2(sum[0], sum[1]));
+        l += total.x + total.y;
         tmem_wait_st();
         fence_before();
         bar_arrive(&sm.p_ready[t]);
