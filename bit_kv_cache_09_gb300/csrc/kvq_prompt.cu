@@ -44,7 +44,7 @@ constexpr float kWeightExp = 7.0f;
 struct Smem {
   uint8_t q[2][kTileBytes2];
   uint8_t kv[kStages][kTileBytes2];
-  uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_ready[2], o_full[2], done;
+  uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_half[2], p_ready[2], o_full[2], done;
   uint32_t tmem;
   int seq, tile, abort;
 };
@@ -93,8 +93,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, const Pro
 }
 
 // One lane of the (converged) warp. Code behind this predicate, and not behind a test of the lane
-// number, issues its MMAs without a loop that makes their operands uniform (75 -> 64 cycles each
-// and less, so that the tensor cores and not the issue set the pace).
+// number, issues its MMAs without a loop that makes their operands uniform: 8 of them take 160 to
+// 310 cycles instead of 600 to 950, more than the 512 that the tensor cores need.
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(is));
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.q_full[i], 1);
       bar_init(&sm.s_full[i], 1);
+      bar_init(&sm.p_half[i], kTile);
       bar_init(&sm.p_ready[i], kTile);
       bar_init(&sm.o_full[i], 1);
     }
@@ -372,17 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && j < n[t]) {
-              ok = bar_wait(&sm.p_ready[t], j & 1, p, sm);
-              if (ok) {
-                fence_after();
-                const int steps = (n_keys[t] - j * kTile + 15) / 16;
+              const int steps = (n_keys[t] - j * kTile + 15) / 16;
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                  if (s < steps)
-                    mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + s * 8, v_desc + s * (2048 >> 4), idesc<BF16>(true),
-                           j > 0 || s > 0);
-                if (j == n[t] - 1) mma_commit(&sm.o_full[t]);
+              for (int half = 0; half < 2; ++half) {  // the first 64 keys while the weights of the others are made
+                if (ok) ok = bar_wait(half ? &sm.p_ready[t] : &sm.p_half[t], j & 1, p, sm);
+                if (ok) {
+                  fence_after();
+#pragma unroll
+                  for (int s = half * 4; s < half * 4 + 4; ++s)
+                    if (s < steps)
+                      mma_ts(tmem + 256 + t * kTile, tmem + t * kTile + s * 8, v_desc + s * (2048 >> 4), idesc<BF16>(true),
+                             j > 0 || s > 0);
+                }
               }
+              if (ok && j == n[t] - 1) mma_commit(&sm.o_full[t]);
             }
             if (ok && j + 1 < n[t]) {
               ok = bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm);
@@ -471,6 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[c / 2] = pack2<BF16>(a, b);
           }
           tmem_st16(s_addr + c0 / 2, w);
+          if (c0 == 32) {
+            tmem_wait_st();
+            fence_before();
+            bar_arrive(&sm.p_half[t]);
+          }
         }
         const float2 total = split(add2(sum[0], sum[1]));
         l += total.x + total.y;
