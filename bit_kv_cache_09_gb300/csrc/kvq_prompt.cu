@@ -87,7 +87,7 @@ __device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint
   }
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, const PromptParams& p, Smem& sm) {
-  for (int i = 0; i < 32; ++i)
+  for (int i = 0; i < 8; ++i)
     if (bar_try(b, parity)) return true;
   return bar_wait_slow(b, parity, p.wait_ns, &sm.abort, p.err);
 }
@@ -213,6 +213,51 @@ __device__ __forceinline__ Span span_of(const PromptParams& p, int s) {
   return x;
 }
 
+// How many pairs of query tiles a sequence has.
+__device__ __forceinline__ int pairs_of(const PromptParams& p, int s, int tokens) {
+  return s < p.n_seqs ? (span_of(p, s).lq + 2 * tokens - 1) / (2 * tokens) : 0;
+}
+
+// Sequence and pair of tiles of item `want` (all lanes); false: there are fewer. Causal rows further
+// back see more keys, so late pairs come first: over all sequences where a lane can hold one
+// each, sequence by sequence where there are more.
+__device__ __forceinline__ bool find_pair(const PromptParams& p, int want, int tokens, int& seq, int& tile) {
+  const int lane = threadIdx.x & 31;
+  if (p.n_seqs <= 32) {
+    const int n = pairs_of(p, lane, tokens);
+    auto from = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, n - level)); };
+    if (from(0) <= want) return false;
+    int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)n);  // from(lo) > want >= from(hi) = 0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > want) lo = mid; else hi = mid;
+    }
+    tile = lo;
+    want -= from(lo + 1);
+    uint32_t have = __ballot_sync(0xffffffffu, n > lo);
+    for (; want > 0; --want) have &= have - 1;
+    seq = __ffs(have) - 1;
+    return true;
+  }
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+    int sum = pairs_of(p, s0 + lane, tokens);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, sum > want);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      seq = s0 + l;
+      tile = __shfl_sync(0xffffffffu, sum - 1, l) - want;
+      return true;
+    }
+    want -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -244,26 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_allow_dependents();
-  if (warp == 0) {  // which sequence, and which of its pairs of tiles (the longest rows first)
-    int want = blockIdx.x / p.H, seq = -1, tile = 0;
-    for (int s0 = 0; s0 < p.n_seqs && seq < 0; s0 += 32) {
-      const int s = s0 + lane;
-      const int n = s < p.n_seqs ? (span_of(p, s).lq + 2 * tokens - 1) / (2 * tokens) : 0;
-      int sum = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, sum > want);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        seq = s0 + l;
-        tile = __shfl_sync(0xffffffffu, sum - 1, l) - want;
-      } else {
-        want -= __shfl_sync(0xffffffffu, sum, 31);
-      }
-    }
+  if (warp == 0) {
+    int seq = -1, tile = 0;
+    if (!find_pair(p, blockIdx.x / p.H, tokens, seq, tile)) seq = -1;
     if (lane == 0) {
       sm.seq = seq;
       sm.tile = tile;
@@ -370,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           const uint64_t v_desc = desc_cols(kv_addr + sv * kTileBytes2);
+          bool have_k = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && j < n[t]) {
@@ -389,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ok && j == n[t] - 1) mma_commit(&sm.o_full[t]);
             }
             if (ok && j + 1 < n[t]) {
-              ok = bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm);
+              if (!have_k) ok = bar_wait(&sm.kv_full[sk], (ck / kStages) & 1, p, sm);
+              have_k = true;
               if (ok) scores(t, sk);
             }
           }
@@ -494,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && t0 + t * tokens < sp.lq) {
         const float inv = see > 0 ? 1.0f / l : 0.0f;
         const int64_t at = sp.q0 + token;
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
 #pragma unroll
         for (int c = 0; c < kDim; c += 32) {
           uint32_t o[32];
@@ -507,9 +538,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               y[i] = see > 0 ? pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
-            uint4* out = reinterpret_cast<uint4*>(p.out + at * p.out_stride + head * kDim + c);
+            uint16_t* out = p.out + at * p.out_stride + head * kDim + c;
+            if (wide) {  // whole 32-byte sectors
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              for (int k = 0; k < 16; k += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + k * 2), KVQ_W4(y, k),
+                             KVQ_W4(y, k + 4) : "memory");
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<uint4*>(out + k * 2) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+            }
           }
         }
         if (p.lse && mine)
