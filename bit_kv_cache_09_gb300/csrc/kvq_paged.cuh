@@ -115,7 +115,7 @@ struct PagedAppendParams {
   const int32_t* block_table;
   const int32_t* lens;
   const int32_t* q_start;
-  const int2* units;
+  const int4* units;
   uint32_t* status;
   const uint16_t* k;
   const uint16_t* v;

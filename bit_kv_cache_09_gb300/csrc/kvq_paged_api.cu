@@ -23,7 +23,7 @@ bool bufs_ok(const kvq_paged_buffers* b) {
 
 bool step_ok(const kvq_paged_step* s) {
   return s && aligned(s->lens, 4) && aligned(s->free_count, 4) && aligned(s->q_start, 4) && aligned(s->positions, 4) &&
-         aligned(s->slots, 4) && aligned(s->units, 8) && aligned(s->tile_start, 4) && aligned(s->status, 4);
+         aligned(s->slots, 4) && aligned(s->units, 16) && aligned(s->tile_start, 4) && aligned(s->status, 4);
 }
 
 bool stride_ok(int64_t stride) { return stride >= 0 && stride < (int64_t(1) << 31) && stride % 8 == 0; }
@@ -92,7 +92,7 @@ kvq_status kvq_paged_append(const kvq_paged_config* cfg, const kvq_paged_buffers
   p.block_table = block_table;
   p.lens = step->lens;
   p.q_start = step->q_start;
-  p.units = reinterpret_cast<const int2*>(step->units);
+  p.units = reinterpret_cast<const int4*>(step->units);
   p.status = step->status;
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);

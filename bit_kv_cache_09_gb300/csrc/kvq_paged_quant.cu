@@ -19,10 +19,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRowThreads = 16;                      // threads of a row, 8 channels each
-constexpr int kRowsPass = kThreads / kRowThreads;    // rows of a pass
-constexpr int kCodeStride = kPagedDim + 8;           // bytes of a staged row of codes
+constexpr int kChunkStride = 528;  // bytes of a staged 512-byte chunk of a tile: shifts its banks by 4 words
 
 template <bool BF16>
 __device__ __forceinline__ float2 to_float2(uint32_t w) {
@@ -30,8 +27,8 @@ __device__ __forceinline__ float2 to_float2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Largest magnitude of the CTA's entries, from the largest bit pattern without the sign
-// (infinities and NaN order above every number).
+// Scale of a block from its entries' largest bit pattern without the sign (infinities and NaN order
+// above every number).
 template <bool BF16>
 __device__ __forceinline__ float scale_of(uint32_t abs_bits, float top) {
   const uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
@@ -40,221 +37,380 @@ __device__ __forceinline__ float scale_of(uint32_t abs_bits, float top) {
   return amax == 0.0f ? 1.0f : fmaxf(__fdiv_rn(amax, top), 1.17549435e-38f);
 }
 
-template <int FMT>
-__device__ __forceinline__ uint32_t code_of(float x, float scale) {
-  const float y = __fdiv_rn(x, scale);
-  if (FMT == KVQ_PAGED_INT8) return (uint32_t)(max(-127, min(127, __float2int_rn(y))) + 128);
-  return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+// x / s in binary32, rounded to nearest. With inv = RN(1/s), x inv is within 2 units in the last
+// place of x / s; one correction by the exact remainder x - q s brings it within one, and Markstein's
+// theorem (IBM J. Res. Dev. 34, 1990: a quotient within one unit, corrected once more with a
+// correctly rounded reciprocal, is the correctly rounded quotient) makes the next one exact. The
+// remainders are exact while nothing underflows: scales below 2^-60 or above 2^100 take the
+// division itself.
+struct Divisor {
+  float s;
+  uint64_t s2, inv2;  // -s and 1/s, twice
+  bool plain;
+};
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 split(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ Divisor divisor(float s) {
+  const float inv = __frcp_rn(s);
+  return Divisor{s, both(-s, -s), both(inv, inv), !(s >= 8.673617379884035e-19f && s <= 1.2676506002282294e30f)};
+}
+// Two quotients at a time (two binary32 operations per instruction).
+__device__ __forceinline__ float2 quotient(float2 f, const Divisor& d) {
+  const uint64_t x = both(f.x, f.y);
+  uint64_t q = fma2(x, d.inv2, 0ull);  // + 0: the rounded product
+  q = fma2(fma2(q, d.s2, x), d.inv2, q);
+  return split(fma2(fma2(q, d.s2, x), d.inv2, q));
 }
 
+// Codes of four quotients, one per byte. int8: |y| <= 127 + 2^-16, so adding 1.5 2^23 + 128 leaves
+// rint(y) + 128 in the low byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+  if (FMT == KVQ_PAGED_INT8) {
+    const float m = 12583040.0f;
+    const uint32_t x = __float_as_uint(__fadd_rn(a.x, m)), y = __float_as_uint(__fadd_rn(a.y, m));
+    const uint32_t z = __float_as_uint(__fadd_rn(b.x, m)), w = __float_as_uint(__fadd_rn(b.y, m));
+    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+  }
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+         ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
+}
+
+// 8 channels of a row: two words of codes.
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint2 codes8(const uint4& x, const Divisor& d) {
+  float2 y[4] = {to_float2<BF16>(x.x), to_float2<BF16>(x.y), to_float2<BF16>(x.z), to_float2<BF16>(x.w)};
+  if (d.plain) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = make_float2(__fdiv_rn(y[i].x, d.s), __fdiv_rn(y[i].y, d.s));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = quotient(y[i], d);
+  }
+  return make_uint2(codes4<FMT>(y[0], y[1]), codes4<FMT>(y[2], y[3]));
+}
+
+// A thread holds channels 8n .. 8n + 7 of the four rows 16s + {2i, 2i + 1, 2i + 8, 2i + 9}: one
+// operand word of the value tile per channel, or with its neighbour of the other half of 16
+// channels the operand words of the key tile. Keys and values of a unit are two CTAs: a CTA lives
+// for three round trips and the arithmetic of its rows, and what moves is what the resident CTAs
+// hold; with both in one CTA a token of each of 32 requests takes 13.5 us instead of 12.4 (read back
+// included), a batch of prompts the same.
 template <int BT, int FMT, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedAppendParams p) {
-  constexpr int PASSES = BT / kRowsPass;
-  __shared__ __align__(16) uint8_t codes_s[2][BT * kCodeStride];
-  __shared__ uint32_t amax_s[2][kThreads / 32];
+__global__ void __launch_bounds__(BT * 4, 1536 / (BT * 4)) paged_append_kernel(const PagedAppendParams p) {
+  constexpr int THREADS = BT * 4, WARPS = THREADS / 32, CHUNKS = BT / 4;  // 512-byte chunks of the block's keys or values
+  __shared__ __align__(16) uint8_t stage[CHUNKS * kChunkStride];
+  __shared__ uint32_t amax_s[WARPS];
   pdl_wait();
   pdl_allow_dependents();
   const int unit = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  if (unit == 0 && h == 0 && tid == 0 && p.q_start[p.R] > p.n_rows) atomicOr(&p.status[0], KVQ_PAGED_ERR_ROWS);
-  if (unit >= (int)p.status[1]) return;
-  const int2 u = p.units[unit];
-  const int row = u.x, block = u.y;
+  const bool key = blockIdx.z == 0;
+  const uint32_t n_units = p.status[1];
+  const int4 u = p.units[unit];  // within the list whether the step has that many or not
+  if (unit == 0 && h == 0 && key && tid == 0 && p.q_start[p.R] > p.n_rows) atomicOr(&p.status[0], KVQ_PAGED_ERR_ROWS);
+  if (unit >= (int)n_units) return;
+  const int row = u.x, block = u.y, q0 = u.z, before = u.w;
   if (row < 0 || row >= p.R) return;
-  const int q0 = p.q_start[row], n_new = p.q_start[row + 1] - q0;
-  const int after = p.lens[row], before = after - n_new;
+  const int after = p.lens[row];
   const int full0 = before / BT, full1 = after / BT;
   uint16_t* tail = p.tails + ((int64_t)row * p.H + h) * (p.tails_head / 2);
-  const int rt = tid / kRowThreads, c0 = (tid % kRowThreads) * 8;
-  const int64_t head_off = (int64_t)h * kPagedDim + c0;
+  const int n = tid & 15, i = (tid >> 4) & 3, s = tid >> 6;
+  const uint16_t* src = (key ? p.k : p.v) + h * kPagedDim + n * 8;
+  const int64_t stride = key ? p.k_stride : p.v_stride;
+  auto tok = [&](int k) { return 16 * s + 2 * i + (k & 1) + (k >> 1) * 8; };  // of the thread's row k
 
   if (block >= 0) {
     const int id = block < p.max_blocks ? p.block_table[(int64_t)row * p.max_blocks + block] : -1;
-    uint4 kx[PASSES], vx[PASSES];
-    uint32_t ka = 0u, va = 0u;
+    uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int t = i * kRowsPass + rt, pos = block * BT + t;
-      kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < 4; ++k) {
+      const int t = tok(k), pos = block * BT + t;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
       if (pos >= before) {
         const int64_t r = (int64_t)q0 + (pos - before);
-        if (r < p.n_rows) {
-          kx[i] = *reinterpret_cast<const uint4*>(p.k + r * p.k_stride + head_off);
-          vx[i] = *reinterpret_cast<const uint4*>(p.v + r * p.v_stride + head_off);
-        }
+        if (r < p.n_rows) x[k] = *reinterpret_cast<const uint4*>(src + r * stride);
       } else {  // kept in the tail since an earlier step
-        const uint16_t* tt = tail + (t / kTileTailTokens) * (kTileBytes / 2);
-        uint32_t* kw = reinterpret_cast<uint32_t*>(&kx[i]);
-        uint32_t* vw = reinterpret_cast<uint32_t*>(&vx[i]);
+        const uint16_t* tt = tail + s * (kTileBytes / 2);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
 #pragma unroll
         for (int c = 0; c < 8; c += 2) {
-          kw[c / 2] = *reinterpret_cast<const uint32_t*>(tt + tile_k_tail(t % kTileTailTokens, c0 + c));
-          vw[c / 2] = (uint32_t)tt[tile_v_tail(t % kTileTailTokens, c0 + c)] |
-                      ((uint32_t)tt[tile_v_tail(t % kTileTailTokens, c0 + c + 1)] << 16);
+          if (key)
+            w[c / 2] = *reinterpret_cast<const uint32_t*>(tt + tile_k_tail(t & 15, n * 8 + c));
+          else
+            w[c / 2] = (uint32_t)tt[tile_v_tail(t & 15, n * 8 + c)] | ((uint32_t)tt[tile_v_tail(t & 15, n * 8 + c + 1)] << 16);
         }
       }
     }
+    uint32_t top_bits = 0u;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(&kx[i]);
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&vx[i]);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[k]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        ka = __vmaxu2(ka, kw[w] & 0x7fff7fffu);
-        va = __vmaxu2(va, vw[w] & 0x7fff7fffu);
-      }
+      for (int c = 0; c < 4; ++c) top_bits = __vmaxu2(top_bits, w[c] & 0x7fff7fffu);
     }
-    ka = max(ka & 0xffffu, ka >> 16);
-    va = max(va & 0xffffu, va >> 16);
-    ka = __reduce_max_sync(0xffffffffu, ka);
-    va = __reduce_max_sync(0xffffffffu, va);
-    if ((tid & 31) == 0) {
-      amax_s[0][tid / 32] = ka;
-      amax_s[1][tid / 32] = va;
-    }
+    top_bits = __reduce_max_sync(0xffffffffu, max(top_bits & 0xffffu, top_bits >> 16));
+    if ((tid & 31) == 0) amax_s[tid / 32] = top_bits;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      ka = max(ka, amax_s[0][w]);
-      va = max(va, amax_s[1][w]);
-    }
-    const float top = FMT == KVQ_PAGED_INT8 ? 127.0f : 448.0f;
-    const float ks = scale_of<BF16>(ka, top), vs = scale_of<BF16>(va, top);
+    for (int w = 0; w < WARPS; ++w) top_bits = max(top_bits, amax_s[w]);
+    const float scale = scale_of<BF16>(top_bits, FMT == KVQ_PAGED_INT8 ? 127.0f : 448.0f);
+    const Divisor d = divisor(scale);
+    uint8_t* tile = stage + (s >> 1) * 8 * kChunkStride;
+    uint2 c[4];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int t = i * kRowsPass + rt;
+    for (int k = 0; k < 4; ++k) c[k] = codes8<FMT, BF16>(x[k], d);
+    if (key) {
+      // this thread keeps two of the four channel pairs of its 16 channels and gets the other half's
+      // codes of those
+      const int odd = n & 1;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(a ? &vx[i] : &kx[i]);
-        const float s = a ? vs : ks;
-        uint32_t o[2] = {0u, 0u};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? c[k].x : c[k].y, 1);
+        const uint32_t lo = odd ? got : c[k].x, hi = odd ? c[k].y : got;  // channels 0..7 and 8..15: pairs 2 odd, 2 odd + 1
+        const int t = tok(k) & 31;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(tile + ((t >> 3) * 2 + (n >> 3)) * kChunkStride +
+                                                    ((t & 7) * 4 + 2 * odd) * 16 + ((n >> 1) & 3) * 4);
+        dst[0] = __byte_perm(lo, hi, 0x5410);
+        dst[4] = __byte_perm(lo, hi, 0x7632);
+      }
+    } else {  // byte k of a word is row k
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = to_float2<BF16>(w[c]);
-          o[c / 2] |= (code_of<FMT>(f.x, s) | (code_of<FMT>(f.y, s) << 8)) << (16 * (c & 1));
-        }
-        *reinterpret_cast<uint2*>(&codes_s[a][t * kCodeStride + c0]) = make_uint2(o[0], o[1]);
+      for (int g = 0; g < 8; ++g) {
+        const uint32_t w0 = g < 4 ? c[0].x : c[0].y, w1 = g < 4 ? c[1].x : c[1].y;
+        const uint32_t w2 = g < 4 ? c[2].x : c[2].y, w3 = g < 4 ? c[3].x : c[3].y;
+        const uint32_t sel = (g & 3) | ((4 + (g & 3)) << 4);
+        *reinterpret_cast<uint32_t*>(tile + (n >> 1) * kChunkStride + (g * 4 + i) * 16 + ((n & 1) * 2 + (s & 1)) * 4) =
+            __byte_perm(__byte_perm(w0, w1, sel), __byte_perm(w2, w3, sel), 0x5410);
       }
     }
     __syncthreads();
     if (id >= 0 && id < p.n_blocks) {
-      uint8_t* out = p.codes + ((int64_t)id * p.H + h) * p.codes_head;
-      for (int i = tid; i < BT * 16; i += kThreads) {  // 16-byte pieces: 256 of keys, 256 of values per tile
-        const int tile = i >> 9, a = (i >> 8) & 1, chunk = (i >> 5) & 7, g = (i >> 2) & 7, l = i & 3;
-        uint32_t w[4];
+      uint8_t* out = p.codes + ((int64_t)id * p.H + h) * p.codes_head + (key ? 0 : kTileBytes / 2);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (a == 0) {  // words of four k16 steps of token 8 (chunk / 2) + g
-            const uint8_t* src = &codes_s[0][(tile * 32 + (chunk >> 1) * 8 + g) * kCodeStride + (chunk & 1) * 64 + k * 16 + l * 2];
-            w[k] = *reinterpret_cast<const uint16_t*>(src) | ((uint32_t)*reinterpret_cast<const uint16_t*>(src + 8) << 16);
-          } else {  // channel 16 chunk + 8 (k / 2) + g of four tokens
-            const uint8_t* src = &codes_s[1][(tile * 32 + (k & 1) * 16 + l * 2) * kCodeStride + chunk * 16 + (k >> 1) * 8 + g];
-            w[k] = src[0] | ((uint32_t)src[kCodeStride] << 8) | ((uint32_t)src[8 * kCodeStride] << 16) |
-                   ((uint32_t)src[9 * kCodeStride] << 24);
-          }
-        }
-        *reinterpret_cast<uint4*>(out + (int64_t)i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      if (tid == 0) {
-        float* sc = p.scales + ((int64_t)id * p.H + h) * 2;
-        sc[0] = ks;
-        sc[1] = vs;
-      }
+      for (int y = tid; y < BT * 8; y += THREADS)  // 256 pieces of 16 bytes from each tile
+        *reinterpret_cast<uint4*>(out + (y >> 8) * kTileBytes + (y & 255) * 16) =
+            *reinterpret_cast<const uint4*>(stage + (y >> 5) * kChunkStride + (y & 31) * 16);
+      if (tid == 0) p.scales[((int64_t)id * p.H + h) * 2 + (key ? 0 : 1)] = scale;
     } else if (tid == 0) {
       atomicOr(&p.status[0], KVQ_PAGED_ERR_TABLE);
     }
   }
   if (block < 0 || block == full0) {  // the request's first unit keeps the rows of the unfinished block
-    const int first = max(before, full1 * BT);
-    for (int pos = first + rt; pos < after; pos += kRowsPass) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = tok(k), pos = full1 * BT + t;
       const int64_t r = (int64_t)q0 + (pos - before);
-      if (r >= p.n_rows) continue;
-      const uint4 kr = *reinterpret_cast<const uint4*>(p.k + r * p.k_stride + head_off);
-      const uint4 vr = *reinterpret_cast<const uint4*>(p.v + r * p.v_stride + head_off);
-      const int t = pos - full1 * BT;
-      uint16_t* tt = tail + (t / kTileTailTokens) * (kTileBytes / 2);
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(&kr);
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(&vr);
+      if (pos < before || pos >= after || r >= p.n_rows) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(src + r * stride);
+      uint16_t* tt = tail + s * (kTileBytes / 2);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
 #pragma unroll
       for (int c = 0; c < 8; c += 2) {
-        *reinterpret_cast<uint32_t*>(tt + tile_k_tail(t % kTileTailTokens, c0 + c)) = kw[c / 2];
-        tt[tile_v_tail(t % kTileTailTokens, c0 + c)] = (uint16_t)vw[c / 2];
-        tt[tile_v_tail(t % kTileTailTokens, c0 + c + 1)] = (uint16_t)(vw[c / 2] >> 16);
+        if (key) {
+          *reinterpret_cast<uint32_t*>(tt + tile_k_tail(t & 15, n * 8 + c)) = w[c / 2];
+        } else {
+          tt[tile_v_tail(t & 15, n * 8 + c)] = (uint16_t)w[c / 2];
+          tt[tile_v_tail(t & 15, n * 8 + c + 1)] = (uint16_t)(w[c / 2] >> 16);
+        }
       }
     }
   }
 }
 
-// Read back: 32 threads per (slot, kv head), 4 channels of the key and of the value each.
-template <int FMT, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_dequant_kernel(const PagedDequantParams p) {
+// Four codes of a word as binary32.
+template <int FMT>
+__device__ __forceinline__ float4 values4(uint32_t w) {
+  if (FMT == KVQ_PAGED_INT8)
+    return make_float4((float)((int)(w & 255u) - 128), (float)((int)((w >> 8) & 255u) - 128),
+                       (float)((int)((w >> 16) & 255u) - 128), (float)((int)(w >> 24) - 128));
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+
+constexpr int kReadSlots = 32;  // list entries of a CTA
+
+// Read back. Where 32 entries of the list are the 32 tokens of a tile in order (the slots of a
+// prompt are, but for its ends), a warp reads the tile as it lies, 16 bytes a lane, and writes
+// whole sectors: 2 channels of a key from each of 4 lanes, or 8 channels of a value from 8. Other
+// entries are gathered one by one. A run may begin up to 31 entries before this CTA's share (it is
+// the earlier CTA's then) or end up to 31 behind it.
+template <int FMT, bool BF16, int THREADS>
+__global__ void __launch_bounds__(THREADS) paged_dequant_kernel(const PagedDequantParams p) {
+  constexpr int kReadWarps = THREADS / 32;
+  constexpr int SPAN = kReadSlots + 64;  // 32 entries on both sides
+  __shared__ int slot_s[SPAN];
+  __shared__ uint32_t next_s[SPAN / 32 + 1];  // bit x: entry x follows entry x - 1 in the same tile
+  __shared__ uint16_t runs[kReadSlots], rest[kReadSlots];
+  __shared__ int n_runs, n_rest;
   pdl_wait();
   pdl_allow_dependents();
-  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (i >= p.n * p.H) return;
-  const int64_t s_i = i / p.H;
-  const int h = (int)(i - s_i * p.H), c0 = (threadIdx.x & 31) * 4;
-  const int64_t slot = p.slots[s_i];
-  float k[4], v[4];
-  const float nan = __int_as_float(0x7fffffff);
-  if (slot >= 0 && slot < (int64_t)p.n_blocks * p.bt) {
-    const int64_t id = slot / p.bt;
-    const int t = (int)(slot - id * p.bt);
-    const uint8_t* tile = p.codes + (id * p.H + h) * p.codes_head + (t / kTileCodeTokens) * kTileBytes;
-    const float2 sc = *reinterpret_cast<const float2*>(p.scales + (id * p.H + h) * 2);
-    for (int c = 0; c < 4; ++c) {
-      const uint8_t a = tile[tile_k_code(t % kTileCodeTokens, c0 + c)], b = tile[tile_v_code(t % kTileCodeTokens, c0 + c)];
-      float fa, fb;
-      if (FMT == KVQ_PAGED_INT8) {
-        fa = (float)((int)a - 128);
-        fb = (float)((int)b - 128);
-      } else {
-        fa = __half2float(__half(__nv_cvt_fp8_to_halfraw(a, __NV_E4M3)));
-        fb = __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-      }
-      k[c] = __fmul_rn(fa, sc.x);
-      v[c] = __fmul_rn(fb, sc.y);
-    }
-  } else if (slot < 0 && -1 - slot < (int64_t)p.R * p.bt) {
-    const int64_t at = -1 - slot, row = at / p.bt;
-    const int t = (int)(at - row * p.bt);
-    const uint16_t* tile = p.tails + (row * p.H + h) * (p.tails_head / 2) + (t / kTileTailTokens) * (kTileBytes / 2);
-    for (int c = 0; c < 4; ++c) {
-      k[c] = to_float2<BF16>(tile[tile_k_tail(t % kTileTailTokens, c0 + c)]).x;
-      v[c] = to_float2<BF16>(tile[tile_v_tail(t % kTileTailTokens, c0 + c)]).x;
-    }
-  } else {
-    for (int c = 0; c < 4; ++c) k[c] = v[c] = nan;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  const int64_t base = (int64_t)blockIdx.x * kReadSlots - 32;  // list index of slot_s[0]
+  const int64_t n_slots = (int64_t)p.n_blocks * p.bt;
+  if (tid == 0) n_runs = n_rest = 0;
+  if (tid < SPAN) {
+    const int64_t x = base + tid;
+    const bool in = x >= 0 && x < p.n;
+    const int slot = in ? p.slots[x] : -1;
+    const int prev = in && x > 0 ? p.slots[x - 1] : -1;
+    slot_s[tid] = slot;
+    const uint32_t bits = __ballot_sync(0xffffffffu, in && slot > 0 && slot < n_slots && (slot & 31) != 0 && slot == prev + 1);
+    if (lane == 0) next_s[warp] = bits;
   }
-  *reinterpret_cast<float4*>(p.k_out + i * kPagedDim + c0) = make_float4(k[0], k[1], k[2], k[3]);
-  *reinterpret_cast<float4*>(p.v_out + i * kPagedDim + c0) = make_float4(v[0], v[1], v[2], v[3]);
+  if (tid == 0) next_s[SPAN / 32] = 0u;
+  __syncthreads();
+  // whether a whole tile begins at entry x of the span
+  auto whole = [&](int x) {
+    if (x < 0 || x >= SPAN - 31 || base + x < 0 || slot_s[x] < 0 || slot_s[x] >= n_slots || (slot_s[x] & 31)) return false;
+    const int y = x + 1;
+    return (__funnelshift_r(next_s[y >> 5], next_s[(y >> 5) + 1], y & 31) & 0x7fffffffu) == 0x7fffffffu;
+  };
+  if (tid < kReadSlots && base + 32 + tid < p.n) {
+    const int x = tid + 32, slot = slot_s[x];
+    if (whole(x)) runs[atomicAdd(&n_runs, 1)] = (uint16_t)x;
+    if (slot < 0 || !whole(x - (slot & 31))) rest[atomicAdd(&n_rest, 1)] = (uint16_t)x;
+  }
+  __syncthreads();
+  const int g = lane >> 2, l = lane & 3;
+  for (int k = warp; k < 4 * n_runs; k += kReadWarps) {  // quarters of tiles: half of the keys or values
+    const int x = runs[k >> 2], slot = slot_s[x], half = (k & 1) * 4;
+    const int64_t id = slot / p.bt;
+    const uint4* tile = reinterpret_cast<const uint4*>(p.codes + (id * p.H + h) * p.codes_head +
+                                                       (slot - id * p.bt) / kTileCodeTokens * kTileBytes) + lane;
+    const float2 sc = *reinterpret_cast<const float2*>(p.scales + (id * p.H + h) * 2);
+    const int64_t step = (int64_t)p.H * kPagedDim, first = ((base + x) * p.H + h) * kPagedDim;
+    uint4 w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = tile[((k & 2) * 4 + half + c) * 32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      const int chunk = half + c;
+      if (!(k & 2)) {
+        float* o = p.k_out + first + ((chunk >> 1) * 8 + g) * step + (chunk & 1) * 64 + l * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 f = values4<FMT>(u[q]);
+          *reinterpret_cast<float2*>(o + q * 16) = make_float2(__fmul_rn(f.x, sc.x), __fmul_rn(f.y, sc.x));
+          *reinterpret_cast<float2*>(o + q * 16 + 8) = make_float2(__fmul_rn(f.z, sc.x), __fmul_rn(f.w, sc.x));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float* o = p.v_out + first + ((q & 1) * 16 + l * 2) * step + (chunk * 2 + (q >> 1)) * 8 + g;
+          const float4 f = values4<FMT>(u[q]);
+          o[0] = __fmul_rn(f.x, sc.y);
+          o[step] = __fmul_rn(f.y, sc.y);
+          o[8 * step] = __fmul_rn(f.z, sc.y);
+          o[9 * step] = __fmul_rn(f.w, sc.y);
+        }
+      }
+    }
+  }
+  const int c0 = lane * 4;
+  for (int k0 = warp; k0 < n_rest; k0 += 4 * kReadWarps) {  // the loads of four entries at a time
+    uint32_t kc[4][2], vc[4][2];  // codes in [0], or 16-bit entries
+    float2 sc[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * kReadWarps;
+      if (k >= n_rest) break;
+      const int64_t slot = slot_s[rest[k]];
+      kc[u][0] = kc[u][1] = vc[u][0] = vc[u][1] = 0u;
+      sc[u] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+      if (slot >= 0 && slot < n_slots) {
+        const int64_t id = slot / p.bt;
+        const int t = (int)(slot - id * p.bt);
+        const uint8_t* tile = p.codes + (id * p.H + h) * p.codes_head + (t / kTileCodeTokens) * kTileBytes;
+        sc[u] = *reinterpret_cast<const float2*>(p.scales + (id * p.H + h) * 2);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          kc[u][0] |= (uint32_t)tile[tile_k_code(t % kTileCodeTokens, c0 + c)] << (8 * c);
+          vc[u][0] |= (uint32_t)tile[tile_v_code(t % kTileCodeTokens, c0 + c)] << (8 * c);
+        }
+      } else if (slot < 0 && -1 - slot < (int64_t)p.R * p.bt) {
+        const int64_t at = -1 - slot, row = at / p.bt;
+        const int t = (int)(at - row * p.bt);
+        const uint16_t* tile = p.tails + (row * p.H + h) * (p.tails_head / 2) + (t / kTileTailTokens) * (kTileBytes / 2);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          kc[u][c >> 1] |= (uint32_t)tile[tile_k_tail(t % kTileTailTokens, c0 + c)] << (16 * (c & 1));
+          vc[u][c >> 1] |= (uint32_t)tile[tile_v_tail(t % kTileTailTokens, c0 + c)] << (16 * (c & 1));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = k0 + u * kReadWarps;
+      if (k >= n_rest) break;
+      const int64_t slot = slot_s[rest[k]];
+      float4 kf, vf;
+      if (slot < 0 && -1 - slot < (int64_t)p.R * p.bt) {
+        const float2 a = to_float2<BF16>(kc[u][0]), b = to_float2<BF16>(kc[u][1]);
+        const float2 c = to_float2<BF16>(vc[u][0]), d = to_float2<BF16>(vc[u][1]);
+        kf = make_float4(a.x, a.y, b.x, b.y);
+        vf = make_float4(c.x, c.y, d.x, d.y);
+      } else {  // outside the cache the scales are NaN
+        kf = values4<FMT>(kc[u][0]);
+        vf = values4<FMT>(vc[u][0]);
+        kf = make_float4(__fmul_rn(kf.x, sc[u].x), __fmul_rn(kf.y, sc[u].x), __fmul_rn(kf.z, sc[u].x), __fmul_rn(kf.w, sc[u].x));
+        vf = make_float4(__fmul_rn(vf.x, sc[u].y), __fmul_rn(vf.y, sc[u].y), __fmul_rn(vf.z, sc[u].y), __fmul_rn(vf.w, sc[u].y));
+      }
+      const int64_t o = ((base + rest[k]) * p.H + h) * kPagedDim + c0;
+      *reinterpret_cast<float4*>(p.k_out + o) = kf;
+      *reinterpret_cast<float4*>(p.v_out + o) = vf;
+    }
+  }
 }
 
 template <int FMT, bool BF16>
 cudaError_t append_bt(const PagedAppendParams& p, dim3 grid, cudaStream_t stream) {
   switch (p.bt) {
-    case 32: return launch_pdl(paged_append_kernel<32, FMT, BF16>, grid, dim3(kThreads), 0, stream, p);
-    case 64: return launch_pdl(paged_append_kernel<64, FMT, BF16>, grid, dim3(kThreads), 0, stream, p);
-    default: return launch_pdl(paged_append_kernel<128, FMT, BF16>, grid, dim3(kThreads), 0, stream, p);
+    case 32: return launch_pdl(paged_append_kernel<32, FMT, BF16>, grid, dim3(128), 0, stream, p);
+    case 64: return launch_pdl(paged_append_kernel<64, FMT, BF16>, grid, dim3(256), 0, stream, p);
+    default: return launch_pdl(paged_append_kernel<128, FMT, BF16>, grid, dim3(512), 0, stream, p);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int64_t max_units, int fmt, int dtype, cudaStream_t stream) {
-  const dim3 grid((unsigned)max_units, (unsigned)p.H);
+  const dim3 grid((unsigned)max_units, (unsigned)p.H, 2);
   if (fmt == KVQ_PAGED_INT8)
     return dtype == KVQ_BF16 ? append_bt<KVQ_PAGED_INT8, true>(p, grid, stream) : append_bt<KVQ_PAGED_INT8, false>(p, grid, stream);
   return dtype == KVQ_BF16 ? append_bt<KVQ_PAGED_E4M3, true>(p, grid, stream) : append_bt<KVQ_PAGED_E4M3, false>(p, grid, stream);
 }
 
+template <int FMT, bool BF16>
+cudaError_t dequant_threads(const PagedDequantParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.n + kReadSlots - 1) / kReadSlots), (unsigned)p.H);
+  // Entries that are gathered one by one take a warp each, a whole tile takes four warps: more warps
+  // shorten a small list, fewer and more CTAs suit a long one (8 heads: 1677 entries 13.6 us with 256
+  // threads against 15.9 with 128 (append before it included), 32778 entries 113.5 against 107.5).
+  if ((int64_t)grid.x * grid.y <= 2048)
+    return launch_pdl(paged_dequant_kernel<FMT, BF16, 256>, grid, dim3(256), 0, stream, p);
+  return launch_pdl(paged_dequant_kernel<FMT, BF16, 128>, grid, dim3(128), 0, stream, p);
+}
+
 cudaError_t launch_paged_dequant(const PagedDequantParams& p, int fmt, int dtype, cudaStream_t stream) {
-  const int64_t ctas = (p.n * p.H + kThreads / 32 - 1) / (kThreads / 32);
-  const dim3 grid((unsigned)ctas), block(kThreads);
   if (fmt == KVQ_PAGED_INT8)
-    return dtype == KVQ_BF16 ? launch_pdl(paged_dequant_kernel<KVQ_PAGED_INT8, true>, grid, block, 0, stream, p)
-                             : launch_pdl(paged_dequant_kernel<KVQ_PAGED_INT8, false>, grid, block, 0, stream, p);
-  return dtype == KVQ_BF16 ? launch_pdl(paged_dequant_kernel<KVQ_PAGED_E4M3, true>, grid, block, 0, stream, p)
-                           : launch_pdl(paged_dequant_kernel<KVQ_PAGED_E4M3, false>, grid, block, 0, stream, p);
+    return dtype == KVQ_BF16 ? dequant_threads<KVQ_PAGED_INT8, true>(p, stream) : dequant_threads<KVQ_PAGED_INT8, false>(p, stream);
+  return dtype == KVQ_BF16 ? dequant_threads<KVQ_PAGED_E4M3, true>(p, stream) : dequant_threads<KVQ_PAGED_E4M3, false>(p, stream);
 }
 
 }  // namespace kvq

@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(const TablesPara
   for (int i = gid; i < (int)base[3]; i += step) {
     const int row = row_of(u0, R, i);
     const bool fills = a0[row + 1] > a0[row];
-    reinterpret_cast<int2*>(p.out.units)[i] = make_int2(row, fills ? p.lens[row] / bt + (i - u0[row]) : -1);
+    const int len = p.lens[row];
+    // request, block to quantize, first packed row and tokens cached before
+    reinterpret_cast<int4*>(p.out.units)[i] = make_int4(row, fills ? len / bt + (i - u0[row]) : -1, q0[row], len);
   }
   for (int i = gid; i < (int)base[0]; i += step) {
     const int row = row_of(q0, R, i);

@@ -70,7 +70,7 @@ class StepTables:
     def __init__(self, cfg: kvq.kvq_paged_config, device):
         units = cfg.max_new // cfg.block_tokens + cfg.n_requests
         sizes = (("lens", cfg.n_requests), ("free_count", 1), ("q_start", cfg.n_requests + 1),
-                 ("positions", cfg.max_new), ("slots", cfg.max_new), ("units", 2 * units),
+                 ("positions", cfg.max_new), ("slots", cfg.max_new), ("units", 4 * units),
                  ("tile_start", cfg.n_requests + 1), ("status", 4))
         for name, n in sizes:
             setattr(self, name, torch.zeros(n, dtype=torch.int32, device=device))

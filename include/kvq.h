@@ -359,7 +359,7 @@ typedef struct {
 } kvq_paged_state;
 
 /* What kvq_paged_step_tables writes for one step and the calls of its layers read (device,
- * 4-byte aligned, units 8-byte). Zero-fill `status` once. */
+ * 4-byte aligned, units 16-byte). Zero-fill `status` once. */
 typedef struct {
   int32_t* lens;        /* [n_requests] tokens after the step */
   int32_t* free_count;  /* [1] free blocks after the step */
@@ -367,7 +367,7 @@ typedef struct {
   int32_t* positions;   /* [max_new] position of each new token in its request */
   int32_t* slots;       /* [max_new] where each new token is kept: block * block_tokens + offset once
                            its block is finished, -1 - (request * block_tokens + offset) in a tail */
-  int32_t* units;       /* [max_new / block_tokens + n_requests][2] work list of the append */
+  int32_t* units;       /* [max_new / block_tokens + n_requests][4] work list of the append */
   int32_t* tile_start;  /* [n_requests + 1] work of the decode attention */
   uint32_t* status;     /* [4] error bits (KVQ_PAGED_ERR_*), number of units, then private */
 } kvq_paged_step;

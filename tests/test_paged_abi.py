@@ -76,7 +76,7 @@ def test_step_tables_refusals(lib):
         assert call(st=_state(**{name: None})) == 1 and call(st=_state(**{name: 4098})) == 1
     for name in ("lens", "free_count", "q_start", "positions", "slots", "units", "tile_start", "status"):
         assert call(sp=_step(**{name: None})) == 1 and call(sp=_step(**{name: 65538})) == 1
-    assert call(sp=_step(units=66820)) == 1  # pairs are 8-byte aligned
+    assert call(sp=_step(units=66824)) == 1  # entries of the work list are 16-byte aligned
     assert call(new=None) == 1 and call(new=4098) == 1 and call(commit=2) == 1
     # the state is read while the step is written
     assert call(sp=_step(lens=4096)) == 1 and call(sp=_step(free_count=16384)) == 1 and call(new=65536) == 1
