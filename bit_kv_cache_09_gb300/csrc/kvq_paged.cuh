@@ -149,6 +149,7 @@ struct PagedDecodeParams {
   int64_t q_stride;
   uint16_t* out;
   int zero_rest;      // rows without new tokens become zeros
+  int early;          // the tables are read before the wait for the previous kernel
   float scale_log2;  // softmax_scale * log2(e)
   int64_t codes_head, tails_head;
   int H, r, R, bt, max_blocks, n_blocks;

@@ -145,13 +145,14 @@ size_t kvq_paged_workspace_size(const kvq_paged_config* cfg) {
 kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs,
                                       const int32_t* block_table, const kvq_paged_step* step, int32_t layer,
                                       const void* q, int64_t q_stride, float softmax_scale, void* out,
-                                      int32_t zero_rest, void* ws, size_t ws_bytes, void* stream) {
+                                      uint32_t flags, void* ws, size_t ws_bytes, void* stream) {
   PagedGeometry g;
   const kvq_status st = kvq::make_paged_geometry(cfg, &g);
   if (st != KVQ_OK) return st;
   if (!bufs_ok(bufs) || !aligned(block_table, 4) || !step_ok(step)) return KVQ_ERR_INVALID_ARG;
   if (layer < 0 || layer >= g.L || !aligned(q, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
   if (!stride_ok(q_stride) || !finite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if (flags & ~(KVQ_PAGED_ZERO_REST | KVQ_PAGED_EARLY_TABLES)) return KVQ_ERR_INVALID_ARG;
   if (!aligned(ws, 256) || ws_bytes < kvq::paged_workspace_bytes(g)) return KVQ_ERR_WORKSPACE;
   kvq::PagedDecodeParams p;
   p.codes = static_cast<const uint8_t*>(bufs->codes) + layer * g.codes_layer;
@@ -165,7 +166,8 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_stride;
   p.out = static_cast<uint16_t*>(out);
-  p.zero_rest = zero_rest != 0;
+  p.zero_rest = (flags & KVQ_PAGED_ZERO_REST) != 0;
+  p.early = (flags & KVQ_PAGED_EARLY_TABLES) != 0;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.codes_head = g.codes_head;
   p.tails_head = g.tails_head;

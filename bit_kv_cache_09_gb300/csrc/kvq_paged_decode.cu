@@ -111,6 +111,7 @@ struct TileInfo {
   int pair;            // request * H + head
   int tokens;          // > 0: a tile of codes; <= 0: minus the tokens of a tail tile
   int flags;           // 1: first tile of its pair, 2: last
+  int block_head;      // of a tile of codes: block * H + head
   float ks, vs;
 };
 
@@ -141,7 +142,7 @@ __device__ __forceinline__ void seek(const PagedDecodeParams& p, RowWindow& w, i
 
 // Tile x of the list for every lane with x < end (all lanes call it, with rising x).
 __device__ __forceinline__ TileInfo tile_info(const PagedDecodeParams& p, RowWindow& w, int x, int end) {
-  TileInfo ti{nullptr, -1, 32, 0, 0.0f, 0.0f};
+  TileInfo ti{nullptr, -1, 32, 0, -1, 0.0f, 0.0f};
   const int v = min(x, end - 1) / p.H;
   int row = 0, t0 = 0, t1 = 1, len = 0;
   for (bool todo = x < end;;) {
@@ -171,11 +172,8 @@ __device__ __forceinline__ TileInfo tile_info(const PagedDecodeParams& p, RowWin
     const int block = t / per;
     const int id = block < p.max_blocks ? p.block_table[(int64_t)row * p.max_blocks + block] : -1;
     if (id >= 0 && id < p.n_blocks) {
-      const int64_t bh = (int64_t)id * p.H + h;
-      ti.src = p.codes + bh * p.codes_head + (t - block * per) * kTileBytes;
-      const float2 sc = *reinterpret_cast<const float2*>(p.scales + bh * 2);
-      ti.ks = sc.x;
-      ti.vs = sc.y;
+      ti.block_head = id * p.H + h;
+      ti.src = p.codes + (int64_t)ti.block_head * p.codes_head + (t - block * per) * kTileBytes;
     } else {
       atomicOr(&p.status[0], KVQ_PAGED_ERR_TABLE);
     }
@@ -185,6 +183,13 @@ __device__ __forceinline__ TileInfo tile_info(const PagedDecodeParams& p, RowWin
     ti.src = p.tails + (int64_t)ti.pair * p.tails_head + tt * kTileBytes;
   }
   return ti;
+}
+
+__device__ __forceinline__ void load_scales(const PagedDecodeParams& p, TileInfo& ti) {
+  if (ti.block_head < 0) return;
+  const float2 sc = *reinterpret_cast<const float2*>(p.scales + (int64_t)ti.block_head * 2);
+  ti.ks = sc.x;
+  ti.vs = sc.y;
 }
 
 __device__ __forceinline__ uint64_t now_ns() {
@@ -228,8 +233,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
     sm.ends[warp] = 0;
   }
   __syncwarp();
-  pdl_wait();
-  pdl_allow_dependents();
+  // With early tables only the lengths and block numbers are read in front of the wait for the
+  // previous kernel, which may still be writing tails, codes, scales and queries.
+  if (!p.early) pdl_wait();
 
   const int H = p.H, r = p.r;
   // one round trip: the number of tiles, and the first rows or samples of the search for this warp's row
@@ -239,6 +245,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
   // at least one tile per warp, so that short lists need no joining across CTAs
   const int ctas = max(1, min((int)gridDim.x, total / kWarps));
   const int cta = blockIdx.x;
+  const int a_cta = (int)((int64_t)total * min(cta, ctas) / ctas), b_cta = (int)((int64_t)total * min(cta + 1, ctas) / ctas);
+  const int x_beg = a_cta + (b_cta - a_cta) * warp / kWarps, x_end = a_cta + (b_cta - a_cta) * (warp + 1) / kWarps;
+  if (p.R > 31 && x_beg < x_end) {
+    int lo = 0, hi = p.R;
+    narrow(lo, hi, x_beg / H, sample);
+    seek(p, window, lo, hi, x_beg / H);
+  }
+  TileInfo next = tile_info(p, window, x_beg + lane, x_end);
+  if (p.early) pdl_wait();
+  pdl_allow_dependents();
   if (p.zero_rest) {  // rows without new tokens, shared out over the CTAs
     for (int row = cta; row < p.R; row += gridDim.x)
       if (p.q_start[row + 1] == p.q_start[row]) {
@@ -247,21 +263,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
       }
   }
   if (cta >= ctas || total == 0) return;
-  const int a_cta = (int)((int64_t)total * cta / ctas), b_cta = (int)((int64_t)total * (cta + 1) / ctas);
-  const int x_beg = a_cta + (b_cta - a_cta) * warp / kWarps, x_end = a_cta + (b_cta - a_cta) * (warp + 1) / kWarps;
-
-  if (p.R > 31 && x_beg < x_end) {
-    int lo = 0, hi = p.R;
-    narrow(lo, hi, x_beg / H, sample);
-    seek(p, window, lo, hi, x_beg / H);
-  }
-  TileInfo next = tile_info(p, window, x_beg + lane, x_end), cur = next;
+  load_scales(p, next);
+  TileInfo cur = next;
   int issue = x_beg, next_base = x_beg, cur_base = x_beg;
   bool dead = false;  // a wait ran out: no more copies, the bookkeeping goes on
   auto issue_one = [&]() {  // starts the copy of tile `issue`
     if (issue - next_base == 32) {
       next_base = issue;
       next = tile_info(p, window, issue + lane, x_end);
+      load_scales(p, next);
     }
     const int first_of = __shfl_sync(0xffffffffu, next.flags, issue - next_base) & 1;
     if (first_of || issue == x_beg) {  // the pair's queries are wanted soon
@@ -537,25 +547,32 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
         ends = ends || sm.ends[next_part >> 1];
       }
       if (warp < r) {
-        auto part_of = [&](int i) {
-          return (i & 1) ? reinterpret_cast<const float*>(sm.ring[i >> 1][0]) : sm.head[i >> 1];
-        };
-        auto is_part = [&](int i) { return ((i & 1) ? sm.pair_tail[i >> 1] : sm.pair_head[i >> 1]) == pair; };
+        // part i of the group is the head part of warp i, but for a tail part that begins it; all loads
+        // are independent of one another
+        const int wa = first >> 1, wb = (next_part - 1) >> 1;
+        float mi[kWarps], li[kWarps];
+        float4 v[kWarps];
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const bool tail = i == wa && (first & 1);
+          const bool is = i >= wa && i <= wb && (tail || sm.pair_head[i] == pair);
+          const float* part = tail ? reinterpret_cast<const float*>(sm.ring[i][0]) : sm.head[i];
+          mi[i] = is ? part[kRows * kPagedDim + warp] : -INFINITY;
+          li[i] = is ? part[kRows * kPagedDim + kRows + warp] : 0.0f;
+          v[i] = is ? *reinterpret_cast<const float4*>(part + warp * kPagedDim + c0) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         float M = -INFINITY, L = 0.0f;
-        for (int i = first; i < next_part; ++i)
-          if (is_part(i)) M = fmaxf(M, part_of(i)[kRows * kPagedDim + warp]);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, mi[i]);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i = first; i < next_part; ++i) {
-          if (!is_part(i)) continue;
-          const float* part = part_of(i);
-          const float mi = part[kRows * kPagedDim + warp];
-          const float w = mi == -INFINITY ? 0.0f : exp2_fast(mi - M);
-          const float4 v = *reinterpret_cast<const float4*>(part + warp * kPagedDim + c0);
-          L = fmaf(w, part[kRows * kPagedDim + kRows + warp], L);
-          acc.x = fmaf(w, v.x, acc.x);
-          acc.y = fmaf(w, v.y, acc.y);
-          acc.z = fmaf(w, v.z, acc.z);
-          acc.w = fmaf(w, v.w, acc.w);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float w = mi[i] == -INFINITY ? 0.0f : exp2_fast(mi[i] - M);
+          L = fmaf(w, li[i], L);
+          acc.x = fmaf(w, v[i].x, acc.x);
+          acc.y = fmaf(w, v[i].y, acc.y);
+          acc.z = fmaf(w, v[i].z, acc.z);
+          acc.w = fmaf(w, v[i].w, acc.w);
         }
         if ((first & 1) && ends) {  // begun and ended in this CTA
           const float inv = 1.0f / L;

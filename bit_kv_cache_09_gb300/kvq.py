@@ -34,6 +34,7 @@ PAGED_FORMATS = {"int8": 0, "e4m3": 1}  # kvq_paged_config.format
 F16, BF16 = 0, 1  # 16-bit types of the paged cache and of the prompt attention
 PAGED_ERR_NEW, PAGED_ERR_LENGTH, PAGED_ERR_BLOCKS, PAGED_ERR_STATE = 1, 2, 4, 8  # bits of step.status[0]
 PAGED_ERR_ROWS, PAGED_ERR_TABLE = 16, 32
+PAGED_ZERO_REST, PAGED_EARLY_TABLES = 1, 2  # flag bits of kvq_paged_decode_attention
 PAGED_ERR_NAMES = {1: "new_tokens below -1 or more than max_new in all", 2: "a request outgrows max_blocks",
                    4: "not enough free blocks", 8: "lengths or free count out of range",
                    16: "fewer key/value rows than the step's new tokens", 32: "a block number outside the pool"}
@@ -158,7 +159,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.kvq_paged_dequantize.restype = ctypes.c_int
         L.kvq_paged_workspace_size.argtypes = [pcfg]
         L.kvq_paged_workspace_size.restype = ctypes.c_size_t
-        L.kvq_paged_decode_attention.argtypes = [pcfg, pbuf, vp, pstep, i32, vp, i64, ctypes.c_float, vp, i32,
+        L.kvq_paged_decode_attention.argtypes = [pcfg, pbuf, vp, pstep, i32, vp, i64, ctypes.c_float, vp,
+                                                 ctypes.c_uint32,
                                                  vp, ctypes.c_size_t, vp]
         L.kvq_paged_decode_attention.restype = ctypes.c_int
         L.kvq_prompt_attention.argtypes = [ctypes.POINTER(kvq_prompt_args), vp, ctypes.c_size_t, vp]
@@ -317,11 +319,11 @@ def kvq_paged_dequantize(cfg: kvq_paged_config, bufs: kvq_paged_buffers, layer: 
 
 
 def kvq_paged_decode_attention(cfg: kvq_paged_config, bufs: kvq_paged_buffers, block_table: int, step: kvq_paged_step,
-                               layer: int, q: int, q_stride: int, softmax_scale: float, out: int, zero_rest: int,
+                               layer: int, q: int, q_stride: int, softmax_scale: float, out: int, flags: int,
                                ws: int, ws_bytes: int, stream: int = 0) -> None:
     _check("kvq_paged_decode_attention",
            load().kvq_paged_decode_attention(ctypes.byref(cfg), ctypes.byref(bufs), block_table, ctypes.byref(step),
-                                             layer, q, q_stride, softmax_scale, out, zero_rest, ws, ws_bytes,
+                                             layer, q, q_stride, softmax_scale, out, flags, ws, ws_bytes,
                                              stream))
 
 

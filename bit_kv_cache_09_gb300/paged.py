@@ -8,6 +8,11 @@ Nothing synchronizes or copies to the host, so a step can be captured in a CUDA 
 Every call runs on the current stream of the cache's device. The cache's own tensors
 (tables, workspace) are written by its calls: calls of one cache object must be ordered,
 on one stream or by events.
+
+``attention`` reads the tables while the kernel before it on the stream finishes, unless that
+kernel is this object's ``step``. A kernel that writes ``tables.lens``, ``tables.tile_start`` or
+``block_table`` outside this object must therefore not directly precede ``attention`` on the same
+stream; pass ``early=False`` after one.
 """
 
 from __future__ import annotations
@@ -59,9 +64,13 @@ def _launch(device, name: str, *args) -> None:
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
             return _launch(device, name, *args)
-    status = getattr(kvq.load(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    status = getattr(kvq.load(), name)(*args, _stream(device))
     if status:
         raise kvq.KVQError(name, status, kvq.kvq_status_string(status))
+
+
+def _stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class StepTables:
@@ -112,6 +121,7 @@ class PagedKVCache:
             self.tables = StepTables(self.cfg, self.device)
             self.ws = torch.zeros(max(kvq.kvq_paged_workspace_size(self.cfg), 256), dtype=torch.uint8,
                                   device=self.device)
+        self._tables_on = None  # the stream of a step() that no other call of this object has followed
         # the arguments that never change
         self._cfg, self._bufs, self._state, self._step = (ctypes.byref(x) for x in (self.cfg, self.bufs, self.state,
                                                                                     self.tables.ptrs))
@@ -127,6 +137,7 @@ class PagedKVCache:
         free_count stay as they were, so the step can be built again."""
         ptr = _ints("new_tokens", new_tokens, self.device, self.cfg.n_requests)
         self._call("kvq_paged_step_tables", self._cfg, self._state, ptr, self._step, int(commit))
+        self._tables_on = _stream(self.device)
         return self.tables
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -139,6 +150,7 @@ class PagedKVCache:
             raise ValueError(f"k has {k.shape[0]} rows, v {v.shape[0]}")
         self._call("kvq_paged_append", self._cfg, self._bufs, self._table, self._step, layer, k.shape[0], k.data_ptr(), ks,
                    v.data_ptr(), vs)
+        self._tables_on = None
 
     def dequantize(self, layer: int, slots: torch.Tensor):
         """Keys and values kept at `slots` (int32, as in StepTables.slots): two float32
@@ -150,7 +162,14 @@ class PagedKVCache:
         self._call("kvq_paged_dequantize", self._cfg, self._bufs, layer, n, ptr, k.data_ptr(), v.data_ptr())
         return k, v
 
-    def attention(self, layer: int, q: torch.Tensor, softmax_scale: float, out: torch.Tensor = None) -> torch.Tensor:
+    def _flags(self, fresh: bool, early) -> int:
+        """Flag bits of an attention call (see the module's docstring)."""
+        if early is None:
+            early = self._tables_on is None or self._tables_on != _stream(self.device)
+        return (kvq.PAGED_ZERO_REST if fresh else 0) | (kvq.PAGED_EARLY_TABLES if early else 0)
+
+    def attention(self, layer: int, q: torch.Tensor, softmax_scale: float, out: torch.Tensor = None,
+                  early=None) -> torch.Tensor:
         """Attention of the newest token of every request in the step. q: [n_requests][n_q][d_head];
         returns out of the same shape. Rows of requests without new tokens keep what `out` held
         (a new `out` holds zeros there)."""
@@ -164,7 +183,8 @@ class PagedKVCache:
         elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous {self.dtype} tensor of shape {tuple(q.shape)} on {self.device}")
         self._call("kvq_paged_decode_attention", self._cfg, self._bufs, self._table, self._step, layer, q.data_ptr(), qs,
-                   softmax_scale, out.data_ptr(), fresh, self._ws, self.ws.numel())
+                   softmax_scale, out.data_ptr(), self._flags(fresh, early), self._ws, self.ws.numel())
+        self._tables_on = None
         return out
 
     def check_errors(self) -> None:

@@ -421,12 +421,17 @@ size_t kvq_paged_workspace_size(const kvq_paged_config* cfg);
  * of finished blocks and the 16-bit rows of the tail. q: row i at element i * q_stride
  * (16-byte aligned, a multiple of 8), its n_kv_heads * gqa_ratio heads behind one another;
  * out [n_requests][n_kv_heads * gqa_ratio][d_head] in the config's dtype (16-byte
- * aligned). Rows of requests without new tokens are left as they were, or, with zero_rest != 0,
- * filled with zeros. */
+ * aligned). Rows of requests without new tokens are left as they were.
+ * flags: KVQ_PAGED_ZERO_REST fills those rows with zeros. KVQ_PAGED_EARLY_TABLES lets the kernel
+ * read step.lens, step.tile_start and block_table while the kernel just before it on `stream` runs
+ * its last thread blocks; the caller guarantees that this one writes none of them (kernels before
+ * it have finished by then). Other bits: KVQ_ERR_INVALID_ARG. */
+#define KVQ_PAGED_ZERO_REST 1u
+#define KVQ_PAGED_EARLY_TABLES 2u
 kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs,
                                       const int32_t* block_table, const kvq_paged_step* step, int32_t layer,
                                       const void* q, int64_t q_stride, float softmax_scale, void* out,
-                                      int32_t zero_rest, void* ws, size_t ws_bytes, void* stream);
+                                      uint32_t flags, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- Attention of whole prompts, packed one behind the other ------------------------- */
 

@@ -101,12 +101,13 @@ def test_append_and_dequantize_refusals(lib):
 
 def test_decode_refusals(lib):
     need = kvq.kvq_paged_workspace_size(cfg())
-    dec = lambda c=None, b=None, table=8192, sp=None, layer=0, q=4096, qs=1024, scale=0.1, out=4096, ws=4096, n=need: (  # noqa: E731
+    dec = lambda c=None, b=None, table=8192, sp=None, layer=0, q=4096, qs=1024, scale=0.1, out=4096, ws=4096, n=need, flags=0: (  # noqa: E731
         lib.kvq_paged_decode_attention(B(c or cfg()), B(b or _bufs()), table, B(sp or _step()), layer, q, qs,
-                                       ctypes.c_float(scale), out, 0, ws, n, None))
+                                       ctypes.c_float(scale), out, flags, ws, n, None))
     assert dec(c=cfg(block_tokens=256)) == 2 and dec(b=_bufs(None)) == 1 and dec(table=4097) == 1
     assert dec(sp=_step(tile_start=None)) == 1 and dec(layer=7) == 1 and dec(q=4104) == 1 and dec(out=None) == 1
     assert dec(qs=1020) == 1 and dec(scale=float("nan")) == 1 and dec(scale=float("inf")) == 1
+    assert dec(flags=4) == 1 and dec(flags=2 ** 31) == 1
     assert dec(ws=None) == 4 and dec(ws=4112) == 4 and dec(n=need - 1) == 4
 
 
@@ -130,6 +131,20 @@ def test_prompt_refusals(lib):
     assert call(lse=4097) == 1 and call(ws=None) == 4 and call(ws=4104) == 4 and call(n=255) == 4
     assert lib.kvq_prompt_attention(None, 4096, 256, None) == 1
     assert call(n_q=0, q=None, out=None) == 0  # nothing to compute
+
+
+def test_tables_are_read_early_unless_a_step_was_the_last_call(monkeypatch):
+    """Host logic of the early-tables flag."""
+    now = [5]
+    monkeypatch.setattr(paged, "_stream", lambda device: now[0])
+    c = paged.PagedKVCache.__new__(paged.PagedKVCache)
+    c.device, c._tables_on = None, None
+    Z, E = kvq.PAGED_ZERO_REST, kvq.PAGED_EARLY_TABLES
+    assert c._flags(True, None) == Z | E and c._flags(False, None) == E
+    c._tables_on = 5  # a step on this stream
+    assert c._flags(False, None) == 0 and c._flags(True, None) == Z and c._flags(False, True) == E
+    now[0] = 6        # another stream waits for the step by an event
+    assert c._flags(False, None) == E and c._flags(False, False) == 0
 
 
 def test_python_callers_check_their_tensors():
