@@ -184,6 +184,8 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   return of(kvq::launch_paged_decode(p, g.fmt, g.dtype, static_cast<cudaStream_t>(stream)));
 }
 
+size_t kvq_prompt_workspace_size(void) { return kvq::prompt_workspace_bytes(); }
+
 kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_bytes, void* stream) {
   if (!a) return KVQ_ERR_INVALID_ARG;
   if (a->n_kv_heads < 1 || a->gqa_ratio < 1 || a->n_seqs < 1 || a->n_q < 0 || a->n_kv < 0) return KVQ_ERR_INVALID_ARG;
@@ -201,7 +203,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   if (a->n_q > 0 && (!aligned(a->q, 16) || !aligned(a->out, 16))) return KVQ_ERR_INVALID_ARG;
   if (a->n_kv > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return KVQ_ERR_INVALID_ARG;
   if (a->lse && !aligned(a->lse, 4)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(ws, 256) || ws_bytes < 256) return KVQ_ERR_WORKSPACE;
+  if (!aligned(ws, 256) || ws_bytes < kvq::prompt_workspace_bytes()) return KVQ_ERR_WORKSPACE;
   if (a->n_q == 0) return KVQ_OK;
   kvq::PromptParams p;
   p.q = static_cast<const uint16_t*>(a->q);
@@ -224,6 +226,8 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   p.zero_rest = a->zero_rest != 0;
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   p.err = static_cast<uint32_t*>(ws);
+  p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kvq::kPromptTickets);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kvq::kPromptParts);
   p.wait_ns = kvq::kDefaultWaitNs;
   return of(kvq::launch_prompt(p, a->dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -36,6 +36,9 @@ constexpr int kThreads = 384;                 // 2 x 4 softmax warps; MMA warp, 
 // Registers of a thread: 168 at launch (384 x 168 = 64512); the softmax warps take 208, the
 // last four give theirs back (8 x 32 x 208 + 4 x 32 x 88 = 64512).
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kMaxParts = 16;                 // CTAs of a split item
+constexpr int kPartTiles = 8;                 // key tiles of a part, at least
+constexpr int kPartFloats = kTile * (kDim + 2);  // of one tile's part: o [128][128], m [128], l [128]
 constexpr float kMoveAt = 8.0f;               // the maximum moves when it grew by 2^8
 // Weights are held times 2^7: with the above below 2^15, and binary16 resolves 2^-31 of the
 // largest weight, so that a long flat tail of the softmax is not lost.
@@ -46,7 +49,7 @@ struct Smem {
   uint8_t kv[kStages][kTileBytes2];
   uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_half[2], p_ready[2], o_full[2], done;
   uint32_t tmem;
-  int seq, tile, abort;
+  int seq, tile, h, part, parts, abort, last;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -156,7 +159,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
       ::"r"(addr), KVQ_W16(x, 0) : "memory");
 }
+// Waits for this thread's loads; then names the registers that they fill, so that nothing that reads
+// those moves in front of the wait.
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+#define KVQ_U4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
+#define KVQ_U16(x, i) KVQ_U4(x, i), KVQ_U4(x, i + 4), KVQ_U4(x, i + 8), KVQ_U4(x, i + 12)
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* x) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; i += 16) asm volatile("" : KVQ_U16(x, i));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -258,7 +271,74 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int want, int t
   return false;
 }
 
+// Rows r0 .. r0 + 3 (of the 256 of both tiles) of a split item, by one warp:
+//   M = max_s m_s, o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s
+// in the order of the parts, four at a time in flight.
 template <bool BF16>
+__device__ __forceinline__ void join_rows(const PromptParams& p, const Span& sp, int h, int t0, int tokens, int slot,
+                                          int parts, int r0) {
+  const int lane = threadIdx.x & 31, t = r0 / kTile, row0 = r0 % kTile;
+  float M[4], L[4];
+  float4 A[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    M[i] = -INFINITY;
+    L[i] = 0.0f;
+    A[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  if (t0 + t * tokens >= sp.lq) return;
+  for (int s0 = 0; s0 < parts; s0 += 4) {
+    float m[4][4], l[4][4];
+    float4 v[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* part = p.parts + (int64_t)((slot + min(s0 + s, parts - 1)) * 2 + t) * kPartFloats;
+        const bool is = s0 + s < parts;
+        m[s][i] = is ? __ldcg(part + kTile * kDim + row0 + i) : -INFINITY;
+        l[s][i] = is ? __ldcg(part + kTile * kDim + kTile + row0 + i) : 0.0f;
+        v[s][i] = __ldcg(reinterpret_cast<const float4*>(part + (row0 + i) * kDim) + lane);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mn = M[i];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) mn = fmaxf(mn, m[s][i]);
+      const float a = M[i] == -INFINITY ? 0.0f : exp2_fast(M[i] - mn);
+      L[i] *= a;
+      A[i] = make_float4(A[i].x * a, A[i].y * a, A[i].z * a, A[i].w * a);
+      M[i] = mn;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        // a part without a key for the row: weight 0, its outputs not even written
+        const bool none = m[s][i] == -INFINITY;
+        const float w = none ? 0.0f : exp2_fast(m[s][i] - mn);
+        L[i] = fmaf(w, l[s][i], L[i]);  // NaN scores leave m at -inf and l NaN
+        A[i].x = none ? A[i].x : fmaf(w, v[s][i].x, A[i].x);
+        A[i].y = none ? A[i].y : fmaf(w, v[s][i].y, A[i].y);
+        A[i].z = none ? A[i].z : fmaf(w, v[s][i].z, A[i].z);
+        A[i].w = none ? A[i].w : fmaf(w, v[s][i].w, A[i].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + i, token = t0 + t * tokens + row / p.r, head = h * p.r + row % p.r;
+    if (row >= tokens * p.r || token >= sp.lq) continue;
+    const bool none = M[i] == -INFINITY && L[i] == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / L[i];
+    const int64_t at = sp.q0 + token;
+    *reinterpret_cast<uint2*>(p.out + at * p.out_stride + head * kDim + lane * 4) =
+        make_uint2(pack2<BF16>(A[i].x * inv, A[i].y * inv), pack2<BF16>(A[i].z * inv, A[i].w * inv));
+    if (p.lse && lane == 0)
+      p.lse[at * (p.H * p.r) + head] = none ? -INFINITY : (M[i] - kWeightExp + log2f(L[i])) * 0.6931471805599453f;
+  }
+}
+
+// SPLIT: items may be split along the keys (a template parameter: with the join in it the kernel for
+// whole items takes 361 instead of 342 us for 8192 tokens of 32 heads).
+template <bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
@@ -266,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens = kTile / p.r;  // of a query tile
-  const int h = blockIdx.x % p.H;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.q_full[i], 1);
@@ -290,11 +369,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_allow_dependents();
   if (warp == 0) {
-    int seq = -1, tile = 0;
-    if (!find_pair(p, blockIdx.x / p.H, tokens, seq, tile)) seq = -1;
+    // Items (pairs of tiles of a kv head) in order. Where they would leave half of the SMs without
+    // work, they are split along the keys, into `parts` CTAs each.
+    int item = blockIdx.x, part = 0, parts = 1, seq = -1, tile = 0;
+    if (SPLIT) {
+      const int items = (int)__reduce_add_sync(0xffffffffu, (unsigned)pairs_of(p, lane, tokens)) * p.H;
+      if (items > 0 && 2 * items <= kPromptSplit) {
+        parts = min(kPromptSplit / items, kMaxParts);
+        part = item % parts;
+        item /= parts;
+      }
+    }
+    if (!find_pair(p, item / p.H, tokens, seq, tile)) seq = -1;
     if (lane == 0) {
       sm.seq = seq;
       sm.tile = tile;
+      sm.h = item % p.H;
+      sm.part = part;
+      sm.parts = parts;
     }
   }
   if (p.zero_rest) {  // rows of no sequence, shared out over the CTAs
@@ -311,9 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sm.tmem;
-  const int seq = sm.seq;
+  const int seq = sm.seq, h = sm.h;
+  int parts = 1, slot = 0;  // of a split item; place of this CTA's part in the workspace
+  Span sp{0, 0, 0, 0};
   if (seq >= 0) {
-    const Span sp = span_of(p, seq);
+    sp = span_of(p, seq);
     const int t0 = sm.tile * 2 * tokens;  // first token, within the sequence
     const int shift = sp.lk - sp.lq;      // causal: token i sees keys 0 .. i + shift
     int n_keys[2], n[2];                  // keys that some row of the tile sees, key tiles
@@ -323,7 +417,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       n_keys[t] = beg >= sp.lq ? 0 : p.causal ? min(max(end + shift, 0), sp.lk) : sp.lk;
       n[t] = (n_keys[t] + kTile - 1) / kTile;
     }
-    const int n_max = max(n[0], n[1]);
+    int n_max = max(n[0], n[1]);
+    const int see_all = sp.lk;
+    int first_key = 0;
+    if (SPLIT && sm.parts > 1) {  // this CTA's share of the key tiles; the rest of it counts keys from there
+      parts = max(1, min(sm.parts, n_max / kPartTiles));
+      const int part = sm.part, j0 = part < parts ? n_max * part / parts : 0, j1 = part < parts ? n_max * (part + 1) / parts : 0;
+      slot = blockIdx.x;  // parts of an item have neighbouring slots, all below kPromptSplit
+      first_key = j0 * kTile;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        n_keys[t] = min(max(n_keys[t] - first_key, 0), (j1 - j0) * kTile);
+        n[t] = (n_keys[t] + kTile - 1) / kTile;
+      }
+      n_max = max(n[0], n[1]);
+      sp.k0 += first_key;
+      sp.lk -= first_key;
+      if (part >= parts) parts = 0;  // fewer key tiles than parts: this CTA has none
+    }
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kTmaWarp) {
@@ -442,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = t0 + t * tokens + row / p.r, head = h * p.r + row % p.r;
       const bool mine = row < tokens * p.r && token < sp.lq;
       // keys this row sees (rows of no token: as many as the tile, nothing to mask)
-      const int see = !mine ? n[t] * kTile : p.causal ? min(max(token + 1 + shift, 0), sp.lk) : sp.lk;
+      const int see = !mine ? n[t] * kTile : (p.causal ? min(max(token + 1 + shift, 0), see_all) : see_all) - first_key;
       const float scale = p.scale_log2;
       float m = -INFINITY, l = 0.0f;  // m: maximum in use, of scale * s
       bool ok = true;
@@ -453,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[kTile];
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, x + c);
-        tmem_wait_ld();
+        tmem_wait_ld<kTile>(x);
         const int left = see - j * kTile;  // visible keys of this tile
         if (__any_sync(0xffffffffu, left < kTile) || scale == 0.0f) {
 #pragma unroll
@@ -485,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kDim; c += 16) {
             uint32_t o[16];
             tmem_ld16(o_addr + c, o);
-            tmem_wait_ld();
+            tmem_wait_ld<16>(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st16(o_addr + c, o);
@@ -521,7 +632,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, bar_wait(&sm.o_full[t], 0, p, sm));
         fence_after();
       }
-      if (ok && t0 + t * tokens < sp.lq) {
+      if (SPLIT && ok && parts > 1 && t0 + t * tokens < sp.lq) {  // a part: binary32, joined below
+        float* part = p.parts + (int64_t)(slot * 2 + t) * kPartFloats;
+#pragma unroll
+        for (int c = 0; c < kDim; c += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          if (n[t] > 0) {
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld<32>(o);
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(part + row * kDim + c + k), KVQ_W4(o, k),
+                           KVQ_W4(o, k + 4) : "memory");
+          }
+        }
+        part[kTile * kDim + row] = m;
+        part[kTile * kDim + kTile + row] = l;
+      } else if (ok && (!SPLIT || parts == 1) && t0 + t * tokens < sp.lq) {
         const float inv = see > 0 ? 1.0f / l : 0.0f;
         const int64_t at = sp.q0 + token;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
@@ -531,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (n[t] > 0) {
             tmem_ld32(o_addr + c, o);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(o);
           }
           if (mine) {
             uint32_t y[16];
@@ -558,6 +686,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (SPLIT && parts > 1) {  // the last CTA of a split item joins its parts
+    const int first_slot = slot - sm.part;
+    if (threadIdx.x == 0) {
+      uint32_t* ticket = p.tickets + first_slot;
+      uint32_t n;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
+      sm.last = n == (uint32_t)(parts - 1);
+      if (sm.last) *ticket = 0u;  // ready for the next call
+    }
+    __syncthreads();
+    if (sm.last && warp < 8) {  // the warps that have the registers for it
+      const int t0 = sm.tile * 2 * tokens;
+      for (int r0 = warp * 4; r0 < 2 * kTile; r0 += 32) join_rows<BF16>(p, sp, h, t0, tokens, first_slot, parts, r0);
+    }
+  }
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -591,7 +734,7 @@ bool make_map(EncodeFn fn, CUtensorMap* map, const void* p, int heads, int64_t r
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16>
+template <bool BF16, bool SPLIT>
 cudaError_t launch(const PromptParams& p, int64_t ctas, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    cudaStream_t stream) {
   constexpr int smem = (int)sizeof(Smem) + 1024;
@@ -600,14 +743,17 @@ cudaError_t launch(const PromptParams& p, int64_t ctas, const CUtensorMap& q, co
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(prompt_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(prompt_kernel<BF16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
   }
-  return launch_pdl(prompt_kernel<BF16>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, q, k, v);
+  return launch_pdl(prompt_kernel<BF16, SPLIT>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, q, k, v);
 }
 
 }  // namespace
+
+size_t prompt_workspace_bytes() { return kPromptParts + sizeof(float) * kPromptSplit * 2 * kPartFloats; }
+
 
 cudaError_t launch_prompt(const PromptParams& p, int dtype, cudaStream_t stream) {
   const EncodeFn fn = encode_fn();
@@ -621,7 +767,12 @@ cudaError_t launch_prompt(const PromptParams& p, int dtype, cudaStream_t stream)
   // pairs of tiles: one per 2 * tokens tokens of a sequence, at least one for a sequence with a token
   const int64_t ctas = (p.n_q / (2 * tokens) + std::min(p.n_q, p.n_seqs)) * (int64_t)p.H;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  return dtype == KVQ_BF16 ? launch<true>(p, ctas, q, k, v, stream) : launch<false>(p, ctas, q, k, v, stream);
+  // Few query rows over many keys: one item per CTA would leave SMs idle. The items are counted on the
+  // device; here only what they cannot exceed is known.
+  if (ctas <= kPromptSplit && p.n_seqs <= 32 && p.n_kv >= 2 * kPartTiles * kTile)
+    return dtype == KVQ_BF16 ? launch<true, true>(p, kPromptSplit, q, k, v, stream)
+                             : launch<false, true>(p, kPromptSplit, q, k, v, stream);
+  return dtype == KVQ_BF16 ? launch<true, false>(p, ctas, q, k, v, stream) : launch<false, false>(p, ctas, q, k, v, stream);
 }
 
 }  // namespace kvq

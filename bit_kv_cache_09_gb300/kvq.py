@@ -29,7 +29,7 @@ EXPORTED = ("kvq_buffer_sizes", "kvq_quantize_append", "kvq_dequantize", "kvq_de
             "kvq_version", "kvq_decode_attention_noalloc", "kvq_decode_step", "kvq_decode_attention_ex",
             "kvq_decode_step_ex", "kvq_decode_error", "kvq_decode_noalloc_error", "kvq_paged_buffer_sizes",
             "kvq_paged_step_tables", "kvq_paged_append", "kvq_paged_dequantize", "kvq_paged_workspace_size",
-            "kvq_paged_decode_attention", "kvq_prompt_attention")
+            "kvq_paged_decode_attention", "kvq_prompt_workspace_size", "kvq_prompt_attention")
 PAGED_FORMATS = {"int8": 0, "e4m3": 1}  # kvq_paged_config.format
 F16, BF16 = 0, 1  # 16-bit types of the paged cache and of the prompt attention
 PAGED_ERR_NEW, PAGED_ERR_LENGTH, PAGED_ERR_BLOCKS, PAGED_ERR_STATE = 1, 2, 4, 8  # bits of step.status[0]
@@ -163,6 +163,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  ctypes.c_uint32,
                                                  vp, ctypes.c_size_t, vp]
         L.kvq_paged_decode_attention.restype = ctypes.c_int
+        L.kvq_prompt_workspace_size.argtypes = []
+        L.kvq_prompt_workspace_size.restype = ctypes.c_size_t
         L.kvq_prompt_attention.argtypes = [ctypes.POINTER(kvq_prompt_args), vp, ctypes.c_size_t, vp]
         L.kvq_prompt_attention.restype = ctypes.c_int
         L.kvq_status_string.argtypes = [ctypes.c_int]
@@ -325,6 +327,10 @@ def kvq_paged_decode_attention(cfg: kvq_paged_config, bufs: kvq_paged_buffers, b
            load().kvq_paged_decode_attention(ctypes.byref(cfg), ctypes.byref(bufs), block_table, ctypes.byref(step),
                                              layer, q, q_stride, softmax_scale, out, flags, ws, ws_bytes,
                                              stream))
+
+
+def kvq_prompt_workspace_size() -> int:
+    return int(load().kvq_prompt_workspace_size())
 
 
 def kvq_prompt_attention(args: kvq_prompt_args, ws: int, ws_bytes: int, stream: int = 0) -> None:

@@ -18,8 +18,8 @@ from .paged import _code, _ints, _launch, _rows
 class PromptAttention:
     """Causal (or full) attention with grouped heads over packed sequences.
 
-    Holds the 256-byte workspace of the device's error word; calls on several streams may
-    share the object."""
+    Holds the workspace of its calls (about 20 MB): calls that may overlap, on several streams or in
+    graphs replayed at the same time, need an object each."""
 
     def __init__(self, *, n_kv_heads, gqa_ratio, d_head=128, dtype=torch.float16, device="cuda"):
         self.n_kv, self.n_q, self.gqa, self.d_head = n_kv_heads, n_kv_heads * gqa_ratio, gqa_ratio, d_head
@@ -28,7 +28,8 @@ class PromptAttention:
         if device.type != "cuda":
             raise ValueError("the prompt attention runs on a CUDA device")
         self.device = torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
-        self.ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.ws = torch.zeros(kvq.kvq_prompt_workspace_size(), dtype=torch.uint8, device=self.device)
+        self._ws, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, *,
                  softmax_scale: float, kv_start: torch.Tensor = None, causal: bool = True, out: torch.Tensor = None,
@@ -60,7 +61,7 @@ class PromptAttention:
                                    fresh or return_lse, q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
                                    lse.data_ptr() if return_lse else None)
-        _launch(self.device, "kvq_prompt_attention", ctypes.byref(args), self.ws.data_ptr(), 256)
+        _launch(self.device, "kvq_prompt_attention", ctypes.byref(args), self._ws, self._ws_bytes)
         return (out, lse) if return_lse else out
 
     def check_errors(self) -> None:

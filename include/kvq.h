@@ -461,8 +461,12 @@ typedef struct {
   float* lse; /* NULL, or [n_q][n_kv_heads * gqa_ratio]: ln sum exp(softmax_scale * q . k) */
 } kvq_prompt_args;
 
-/* ws: at least 256 bytes of device memory, zero-filled once (error word in its first 4
- * bytes, kvq_decode_error reads it). */
+/* Bytes of workspace of kvq_prompt_attention (about 20 MB): an error word (first 4 bytes,
+ * kvq_decode_error reads it), counters, and the parts of work that is split along the keys when
+ * there are few query rows. Zero-fill it once; every call leaves its counters at zero. Calls that
+ * may overlap need one each. */
+size_t kvq_prompt_workspace_size(void);
+
 kvq_status kvq_prompt_attention(const kvq_prompt_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */

@@ -160,6 +160,33 @@ def test_values_of_one_sequence_stay_in_it(dtype):
             assert torch.equal(got[a:b], want[a:b]) and torch.equal(gl[a:b], wl[a:b])
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,r,H", [
+    ([1], [5000], 4, 2), ([40], [2200], 4, 8), ([64, 1, 30], [4000, 100, 2111], 4, 2), ([300], [2100], 8, 1),
+    ([900], [9000], 4, 8), ([2300], [2300], 4, 8), ([200, 100], [150, 6000], 2, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows_over_many_keys(q_lens, kv_lens, r, H, causal):
+    """Work that is split along the keys and joined; twice, since the counters have to be left at zero."""
+    att, q, k, v, out, lse = run(q_lens, kv_lens=kv_lens, r=r, H=H, seed=12, causal=causal, some=6)
+    again, lse2 = att(q, k, v, starts(q_lens), kv_start=starts(kv_lens), softmax_scale=SCALE, causal=causal, return_lse=True)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    assert not att.ws[256:1024].any()
+
+
+def test_split_work_keeps_nan_and_masked_rows():
+    rng = np.random.default_rng(13)
+    q, k, v = rows(rng, 70, 4, torch.float16), rows(rng, 4000, 1, torch.float16), rows(rng, 4000, 1, torch.float16)
+    att = PromptAttention(n_kv_heads=1, gqa_ratio=4)
+    args = dict(kv_start=starts([4000]), softmax_scale=SCALE, return_lse=True)
+    want, _ = att(q, k, v, starts([70]), **args)
+    k[17] = math.nan  # every row sees it
+    out, lse = att(q, k, v, starts([70]), **args)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    k[17], v[3999] = 0.0, 0.0
+    q[5, 2] = math.nan  # one row
+    out, lse = att(q, k, v, starts([70]), **args)
+    assert torch.isnan(out[5, 2]).all() and torch.isfinite(out[:5]).all() and torch.isfinite(out[6:]).all()
+
+
 def test_bad_starts_do_not_leave_the_rows():
     """Starts beyond the rows or decreasing are clamped: outputs are unspecified there, the other rows stand."""
     rng = np.random.default_rng(10)
@@ -181,9 +208,11 @@ def test_streams_and_graph():
     want = att(q, k, v, s, softmax_scale=SCALE)
     torch.cuda.synchronize()
     streams, outs = [torch.cuda.Stream() for _ in range(2)], []
-    for x in streams * 3:
+    each = [PromptAttention(n_kv_heads=2, gqa_ratio=4, dtype=torch.bfloat16) for _ in streams]
+    torch.cuda.synchronize()
+    for x, a in list(zip(streams, each)) * 3:
         with torch.cuda.stream(x):
-            outs.append(att(q, k, v, s, softmax_scale=SCALE))
+            outs.append(a(q, k, v, s, softmax_scale=SCALE))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in outs)
     out, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
