@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(THREADS) paged_dequant_kernel(const PagedDequa
     const int slot = in ? p.slots[x] : -1;
     const int prev = in && x > 0 ? p.slots[x - 1] : -1;
     slot_s[tid] = slot;
-    const uint32_t bits = __ballot_sync(0xffffffffu, in && slot > 0 && slot < n_slots && (slot & 31) != 0 && slot == prev + 1);
+    const uint32_t bits = __ballot_sync(0xffffffffu, in && slot > 0 && slot < n_slots && (slot & 31) != 0 && slot - 1 == prev);
     if (lane == 0) next_s[warp] = bits;
   }
   if (tid == 0) next_s[SPAN / 32] = 0u;

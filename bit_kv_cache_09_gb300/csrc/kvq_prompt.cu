@@ -44,12 +44,18 @@ constexpr float kMoveAt = 8.0f;               // the maximum moves when it grew 
 // largest weight, so that a long flat tail of the softmax is not lost.
 constexpr float kWeightExp = 7.0f;
 
+// A sequence's rows, kept inside the arrays whatever the starts say.
+struct Span {
+  int q0, lq, k0, lk;
+};
+
 struct Smem {
   uint8_t q[2][kTileBytes2];
   uint8_t kv[kStages][kTileBytes2];
   uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_half[2], p_ready[2], o_full[2], done;
   uint32_t tmem;
-  int seq, tile, h, part, parts, abort, last;
+  Span span;
+  int found, tile, h, part, parts, abort, last;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -213,10 +219,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A sequence's rows, kept inside the arrays whatever the starts say.
-struct Span {
-  int q0, lq, k0, lk;
-};
 __device__ __forceinline__ Span span_of(const PromptParams& p, int s) {
   Span x;
   x.q0 = min(max(p.q_start[s], 0), p.n_q);
@@ -227,19 +229,33 @@ __device__ __forceinline__ Span span_of(const PromptParams& p, int s) {
 }
 
 // How many pairs of query tiles a sequence has.
-__device__ __forceinline__ int pairs_of(const PromptParams& p, int s, int tokens) {
-  return s < p.n_seqs ? (span_of(p, s).lq + 2 * tokens - 1) / (2 * tokens) : 0;
-}
+__device__ __forceinline__ int pairs_of(const Span& x, int tokens) { return (x.lq + 2 * tokens - 1) / (2 * tokens); }
 
-// Sequence and pair of tiles of item `want` (all lanes); false: there are fewer. Causal rows further
-// back see more keys, so late pairs come first: over all sequences where a lane can hold one
-// each, sequence by sequence where there are more.
-__device__ __forceinline__ bool find_pair(const PromptParams& p, int want, int tokens, int& seq, int& tile) {
+// Sequence, its rows and pair of tiles of item `want` of `parts` parts each (all lanes; SPLIT: parts and
+// part are set, else 1 and 0); false: there are fewer. Causal rows further back see more keys, so late
+// pairs come first: over all sequences where a lane can hold one each, sequence by sequence where
+// there are more.
+template <bool SPLIT>
+__device__ __forceinline__ bool find_pair(const PromptParams& p, int item, int tokens, Span& sp, int& tile, int& h, int& part,
+                                          int& parts) {
   const int lane = threadIdx.x & 31;
+  part = 0;
+  parts = 1;
   if (p.n_seqs <= 32) {
-    const int n = pairs_of(p, lane, tokens);
+    Span x{0, 0, 0, 0};
+    if (lane < p.n_seqs) x = span_of(p, lane);
+    const int n = pairs_of(x, tokens);
     auto from = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, n - level)); };
-    if (from(0) <= want) return false;
+    const int pairs = from(0);
+    // Where whole items would leave half of the SMs without work, they are split along the keys.
+    if (SPLIT && pairs > 0 && 2 * pairs * p.H <= kPromptSplit) {
+      parts = min(kPromptSplit / (pairs * p.H), kMaxParts);
+      part = item % parts;
+      item /= parts;
+    }
+    int want = item / p.H;
+    h = item - want * p.H;
+    if (pairs <= want) return false;
     int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)n);  // from(lo) > want >= from(hi) = 0
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -249,11 +265,17 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int want, int t
     want -= from(lo + 1);
     uint32_t have = __ballot_sync(0xffffffffu, n > lo);
     for (; want > 0; --want) have &= have - 1;
-    seq = __ffs(have) - 1;
+    const int l = __ffs(have) - 1;
+    sp = Span{__shfl_sync(0xffffffffu, x.q0, l), __shfl_sync(0xffffffffu, x.lq, l), __shfl_sync(0xffffffffu, x.k0, l),
+              __shfl_sync(0xffffffffu, x.lk, l)};
     return true;
   }
+  int want = item / p.H;
+  h = item - want * p.H;
   for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-    int sum = pairs_of(p, s0 + lane, tokens);
+    Span x{0, 0, 0, 0};
+    if (s0 + lane < p.n_seqs) x = span_of(p, s0 + lane);
+    int sum = pairs_of(x, tokens);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, off);
@@ -262,8 +284,9 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int want, int t
     const uint32_t hit = __ballot_sync(0xffffffffu, sum > want);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      seq = s0 + l;
       tile = __shfl_sync(0xffffffffu, sum - 1, l) - want;
+      sp = Span{__shfl_sync(0xffffffffu, x.q0, l), __shfl_sync(0xffffffffu, x.lq, l), __shfl_sync(0xffffffffu, x.k0, l),
+                __shfl_sync(0xffffffffu, x.lk, l)};
       return true;
     }
     want -= __shfl_sync(0xffffffffu, sum, 31);
@@ -362,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kTmaWarp && lane < 3) {
+    const CUtensorMap* map = lane == 0 ? &q_map : lane == 1 ? &k_map : &v_map;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -369,22 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_allow_dependents();
   if (warp == 0) {
-    // Items (pairs of tiles of a kv head) in order. Where they would leave half of the SMs without
-    // work, they are split along the keys, into `parts` CTAs each.
-    int item = blockIdx.x, part = 0, parts = 1, seq = -1, tile = 0;
-    if (SPLIT) {
-      const int items = (int)__reduce_add_sync(0xffffffffu, (unsigned)pairs_of(p, lane, tokens)) * p.H;
-      if (items > 0 && 2 * items <= kPromptSplit) {
-        parts = min(kPromptSplit / items, kMaxParts);
-        part = item % parts;
-        item /= parts;
-      }
-    }
-    if (!find_pair(p, item / p.H, tokens, seq, tile)) seq = -1;
+    Span sp{0, 0, 0, 0};
+    int tile = 0, h = 0, part, parts;
+    const bool found = find_pair<SPLIT>(p, blockIdx.x, tokens, sp, tile, h, part, parts);
     if (lane == 0) {
-      sm.seq = seq;
+      sm.span = sp;
+      sm.found = found;
       sm.tile = tile;
-      sm.h = item % p.H;
+      sm.h = h;
       sm.part = part;
       sm.parts = parts;
     }
@@ -403,11 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sm.tmem;
-  const int seq = sm.seq, h = sm.h;
+  const int h = sm.h;
   int parts = 1, slot = 0;  // of a split item; place of this CTA's part in the workspace
-  Span sp{0, 0, 0, 0};
-  if (seq >= 0) {
-    sp = span_of(p, seq);
+  Span sp = sm.span;
+  if (sm.found) {
     const int t0 = sm.tile * 2 * tokens;  // first token, within the sequence
     const int shift = sp.lk - sp.lq;      // causal: token i sees keys 0 .. i + shift
     int n_keys[2], n[2];                  // keys that some row of the tile sees, key tiles
@@ -653,29 +671,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = see > 0 ? 1.0f / l : 0.0f;
         const int64_t at = sp.q0 + token;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
+        uint32_t o[kDim];
+        if (n[t] > 0) {
 #pragma unroll
-        for (int c = 0; c < kDim; c += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          if (n[t] > 0) {
-            tmem_ld32(o_addr + c, o);
-            tmem_wait_ld<32>(o);
-          }
-          if (mine) {
-            uint32_t y[16];
+          for (int c = 0; c < kDim; c += 32) tmem_ld32(o_addr + c, o + c);
+          tmem_wait_ld<kDim>(o);
+        }
+        if (mine) {
+          uint16_t* out = p.out + at * p.out_stride + head * kDim;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              y[i] = see > 0 ? pack2<BF16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
-            uint16_t* out = p.out + at * p.out_stride + head * kDim + c;
+          for (int c = 0; c < kDim; c += 16) {
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y[i] = see > 0 ? pack2<BF16>(__uint_as_float(o[c + 2 * i]) * inv, __uint_as_float(o[c + 2 * i + 1]) * inv) : 0u;
             if (wide) {  // whole 32-byte sectors
-#pragma unroll
-              for (int k = 0; k < 16; k += 8)
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + k * 2), KVQ_W4(y, k),
-                             KVQ_W4(y, k + 4) : "memory");
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + c), KVQ_W4(y, 0), KVQ_W4(y, 4)
+                           : "memory");
             } else {
-#pragma unroll
-              for (int k = 0; k < 16; k += 4)
-                *reinterpret_cast<uint4*>(out + k * 2) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+              *reinterpret_cast<uint4*>(out + c) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
             }
           }
         }

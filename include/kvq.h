@@ -396,7 +396,9 @@ kvq_status kvq_paged_buffer_sizes(const kvq_paged_config* cfg, size_t bytes[KVQ_
 kvq_status kvq_paged_step_tables(const kvq_paged_config* cfg, const kvq_paged_state* state, const int32_t* new_tokens,
                                  const kvq_paged_step* step, int32_t commit, void* stream);
 
-/* Stores the step's new tokens of one layer. k, v: device rows of the config's dtype, new
+/* Stores the step's new tokens of one layer; once per layer and step, since a request that
+ * finishes a block gets new tail rows in place of those that went into the block (so a step
+ * built with commit == 0 cannot be built again with other tokens after its append). k, v: device rows of the config's dtype, new
  * token i of the packed order (step.q_start) at element i * k_stride, its heads of d_head
  * entries behind one another; n_rows rows may be read (rows beyond the step's tokens are
  * not). 16-byte aligned, strides multiples of 8 elements. */
@@ -442,8 +444,9 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
  * zeros and lse -inf. Element (token, head, c) of q, k, v and out is at token * stride +
  * head * d_head + c; strides are multiples of 8 elements, at least a row of heads and below
  * 2^31, pointers 16-byte aligned, and out and lse rows that belong to no sequence are left as they were (with
- * zero_rest != 0: filled with zeros, lse -inf). Values
- * of one sequence never reach the outputs of another, whatever they are.
+ * zero_rest != 0: filled with zeros, lse -inf). Whatever one sequence holds, it never reaches the
+ * outputs of another. Within a causal sequence an infinity or NaN among the values (not the
+ * keys) may reach queries up to 127 tokens before it, whose weight for it is 0.
  * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
  * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale finite and >= 0. */
 typedef struct {

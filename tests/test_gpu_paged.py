@@ -341,6 +341,49 @@ def test_decode_shapes_of_the_work_split(requests, heads, n):
     cache.check_errors()
 
 
+@pytest.mark.parametrize("n_requests,step", [(33, 1), (900, 31), (3000, 97), (8192, 4001)])
+def test_decode_many_rows_few_in_the_step(n_requests, step):
+    """Rows without new tokens between those with some: the search for a tile's request, over windows and samples."""
+    rng = np.random.default_rng(n_requests)
+    at = list(range(step // 2, n_requests, step))
+    lens = [int(rng.integers(1, 150)) for _ in at]
+    cache = make(n_requests=n_requests, n_kv_heads=1, n_blocks=len(at) * 5, max_blocks=5, max_new=sum(lens))
+    new = [0] * n_requests
+    for i, n in zip(at, lens):
+        new[i] = n
+    cache.step(ints(new))
+    k, v = rows(rng, sum(lens), 1, torch.float16), rows(rng, sum(lens), 1, torch.float16, 0.5)
+    cache.append(0, k, v)
+    q = rows(rng, n_requests, 4, torch.float16, 0.3)
+    out = cache.attention(0, q, SCALE)
+    cache.check_errors()
+    first = np.cumsum([0] + lens)
+    held = [[cached_values(x[a:b].double().cpu().numpy(), 32, "int8").astype(np.float64) for x in (k, v)]
+            for a, b in zip(first, first[1:])]
+    check_rows(out[at], q[at], held, 4, SCALE, torch.float16)
+    rest = torch.ones(n_requests, dtype=torch.bool)
+    rest[at] = False
+    assert not out[rest.cuda()].any()
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of 5 GB whose blocks are taken from its far end, as second layer."""
+    rng = np.random.default_rng(18)
+    n_blocks = 20000
+    cache = make(n_requests=2, n_kv_heads=8, block_tokens=128, n_blocks=n_blocks, max_blocks=20, n_layers=2, max_new=5000)
+    cache.free_list.copy_(torch.arange(n_blocks, dtype=torch.int32, device="cuda"))  # the last block on top
+    held, ref = fill(cache, rng, [1000, 333], layer=1)
+    assert int(cache.block_table[0, 0]) == n_blocks - 1
+    q = rows(rng, 2, 32, torch.float16, 0.3)
+    check_rows(cache.attention(1, q, SCALE), q, held, 4, SCALE, torch.float16)
+    page = cache.block_table[0, :7].long()
+    slots = (page[:, None] * 128 + torch.arange(128, device="cuda")).flatten().int()
+    k, v = cache.dequantize(1, slots)
+    for got, want in ((k, held[0][0]), (v, held[0][1])):
+        assert np.array_equal(got.double().cpu().numpy(), want[:896])
+    cache.check_errors()
+
+
 def test_decode_leaves_other_rows_and_masks_stale_tokens():
     """Requests without new tokens keep their rows; what earlier requests left behind the end of a tail or in
     released blocks (here infinities and NaN) reaches nobody."""
@@ -494,6 +537,38 @@ def test_a_captured_step_is_replayed():
     assert pair[0].lens.tolist() == [n + 40 for n in lens]
     for c in pair:
         c.check_errors()
+
+
+def test_attention_right_after_a_step_and_on_another_stream():
+    """Without an append in between (every request's newest token is cached already): the tables of the step just
+    built, each time other ones; then from a stream that waits for the step."""
+    rng = np.random.default_rng(19)
+    lens = [700, 33, 260, 5]
+    cache = make(n_kv_heads=8, n_blocks=100)
+    held, _ = fill(cache, rng, lens)
+    q = rows(rng, 4, 32, torch.float16, 0.3)
+    want = cache.attention(0, q, SCALE)
+    check_rows(want, q, held, 4, SCALE, torch.float16)
+    other, out = torch.cuda.Stream(), torch.zeros_like(want)
+    cache.lens.zero_()
+    cache.step(ints([0, 0, 0, 0]))
+    for i in range(12):
+        some = [n if (i >> (j % 3)) & 1 else 0 for j, n in enumerate(lens)]
+        new = ints(some)
+        out.zero_()
+        cache.step(new, commit=False)  # lengths `some` over the same blocks
+        if i % 2:
+            other.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(other):
+                cache.attention(0, q, SCALE, out=out)
+            torch.cuda.current_stream().wait_stream(other)
+        else:
+            cache.attention(0, q, SCALE, out=out)
+        late = cache.attention(0, q, SCALE, out=torch.zeros_like(out), early=False)
+        assert torch.equal(out, late)
+        for j, n in enumerate(some):
+            assert bool(out[j].any()) == (n > 0)  # unfinished blocks hold what `fill` left
+    cache.check_errors()
 
 
 @pytest.mark.parametrize("fmt,dtype", [("int8", torch.float16), ("e4m3", torch.bfloat16)])
