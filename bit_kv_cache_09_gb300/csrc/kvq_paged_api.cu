@@ -152,7 +152,7 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   if (!bufs_ok(bufs) || !aligned(block_table, 4) || !step_ok(step)) return KVQ_ERR_INVALID_ARG;
   if (layer < 0 || layer >= g.L || !aligned(q, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
   if (!stride_ok(q_stride) || !finite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
-  if (flags & ~(KVQ_PAGED_ZERO_REST | KVQ_PAGED_EARLY_TABLES)) return KVQ_ERR_INVALID_ARG;
+  if (flags & ~(KVQ_PAGED_ZERO_REST | KVQ_PAGED_EARLY_TABLES | KVQ_PAGED_ZERO_WAIT_LIMIT)) return KVQ_ERR_INVALID_ARG;
   if (!aligned(ws, 256) || ws_bytes < kvq::paged_workspace_bytes(g)) return KVQ_ERR_WORKSPACE;
   kvq::PagedDecodeParams p;
   p.codes = static_cast<const uint8_t*>(bufs->codes) + layer * g.codes_layer;
@@ -180,7 +180,7 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   p.err = static_cast<uint32_t*>(ws);
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kvq::kPagedTickets);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kvq::paged_workspace_parts(g));
-  p.wait_ns = kvq::kDefaultWaitNs;
+  p.wait_ns = (flags & KVQ_PAGED_ZERO_WAIT_LIMIT) ? 0 : kvq::kDefaultWaitNs;
   return of(kvq::launch_paged_decode(p, g.fmt, g.dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -190,6 +190,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   if (!a) return KVQ_ERR_INVALID_ARG;
   if (a->n_kv_heads < 1 || a->gqa_ratio < 1 || a->n_seqs < 1 || a->n_q < 0 || a->n_kv < 0) return KVQ_ERR_INVALID_ARG;
   if ((a->dtype != KVQ_F16 && a->dtype != KVQ_BF16) || (a->causal != 0 && a->causal != 1)) return KVQ_ERR_INVALID_ARG;
+  if (a->flags & ~(KVQ_PROMPT_ZERO_REST | KVQ_PROMPT_ZERO_WAIT_LIMIT)) return KVQ_ERR_INVALID_ARG;
   if (a->d_head != 128 || a->gqa_ratio > 8 || a->n_kv_heads > 255 || a->n_seqs > 65535 || a->n_q >= kMaxRows ||
       a->n_kv >= kMaxRows)
     return KVQ_ERR_UNSUPPORTED;
@@ -223,12 +224,12 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   p.H = a->n_kv_heads;
   p.r = a->gqa_ratio;
   p.causal = a->causal;
-  p.zero_rest = a->zero_rest != 0;
+  p.zero_rest = (a->flags & KVQ_PROMPT_ZERO_REST) != 0;
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   p.err = static_cast<uint32_t*>(ws);
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kvq::kPromptTickets);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kvq::kPromptParts);
-  p.wait_ns = kvq::kDefaultWaitNs;
+  p.wait_ns = (a->flags & KVQ_PROMPT_ZERO_WAIT_LIMIT) ? 0 : kvq::kDefaultWaitNs;
   return of(kvq::launch_prompt(p, a->dtype, static_cast<cudaStream_t>(stream)));
 }
 

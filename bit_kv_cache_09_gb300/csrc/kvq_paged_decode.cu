@@ -198,10 +198,11 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-// Waits for a phase of a stage's barrier, at most wait_ns.
+// Waits for a phase of a stage's barrier, at most wait_ns (0: gives up at once).
 __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, uint64_t wait_ns) {
   uint32_t ok = 0;
   uint64_t t0 = 0;
+  if (wait_ns == 0) return false;
   for (int i = 0;; ++i) {
     asm volatile(
         "{\n.reg .pred q;\nmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\nselp.u32 %0, 1, 0, q;\n}"
@@ -355,8 +356,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
       if (!__all_sync(0xffffffffu, ok)) {
         dead = true;
         if (lane == 0) atomicOr(p.err, KVQ_DECODE_ERR_WAIT_TIMEOUT);
-        for (int y = x; y < issue; ++y)  // let what is in flight land, as long again
-          wait_stage(&sm.bars[warp][(y - x_beg) % kStages], ((y - x_beg) / kStages) & 1, p.wait_ns);
+        for (int y = x; y < issue; ++y)  // let what is in flight land, again with a limit
+          wait_stage(&sm.bars[warp][(y - x_beg) % kStages], ((y - x_beg) / kStages) & 1, kDefaultWaitNs);
       }
     }
     const uint4* tile = reinterpret_cast<const uint4*>(sm.ring[warp][s]) + lane;

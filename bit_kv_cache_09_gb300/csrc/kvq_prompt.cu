@@ -81,6 +81,12 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+__device__ __forceinline__ bool bar_give_up(volatile int* abort, uint32_t* err) {
+  *abort = 1;
+  atomicOr(err, KVQ_DECODE_ERR_WAIT_TIMEOUT);
+  return false;
+}
+
 // Waits for a phase, at most wait_ns or until another warp gave up. The first to give up says so
 // in the error word and to the CTA; every role then leaves its loop.
 __device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint64_t wait_ns, volatile int* abort, uint32_t* err) {
@@ -88,14 +94,12 @@ __device__ __forceinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, uint
   for (;;) {
     if (bar_try(b, parity)) return true;
     if (*abort) return false;
-    if (now_ns() - t0 > wait_ns) {
-      *abort = 1;
-      atomicOr(err, KVQ_DECODE_ERR_WAIT_TIMEOUT);
-      return false;
-    }
+    if (now_ns() - t0 > wait_ns) return bar_give_up(abort, err);
   }
 }
+// A limit of 0 gives up at once.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, const PromptParams& p, Smem& sm) {
+  if (p.wait_ns == 0) return bar_give_up(&sm.abort, p.err);
   for (int i = 0; i < 8; ++i)
     if (bar_try(b, parity)) return true;
   return bar_wait_slow(b, parity, p.wait_ns, &sm.abort, p.err);
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kTmaWarp) {
       if (elect_one() && n_max > 0) {
-        int c = 0, landed = 0;  // key and value tiles sent for; of them, waited for here (after giving up)
+        int c = 0, give_up = 0;  // key and value tiles sent for
         bool ok = true;
         auto load_kv = [&](const CUtensorMap* map, int j) {
           const int s = c % kStages;
@@ -482,12 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_kv(&k_map, j);
           if (ok) load_kv(&v_map, j);
         }
-        if (!ok) {  // let what is in flight land before the CTA may end
-          for (int t = 0; t < 2; ++t)
-            if (n[t] > 0) bar_wait_slow(&sm.q_full[t], 0, p.wait_ns, &landed, p.err);
-          for (int i = max(0, c - kStages); i < c; ++i)
-            bar_wait_slow(&sm.kv_full[i % kStages], (i / kStages) & 1, p.wait_ns, &landed, p.err);
-        }
+        // Everything has landed before the CTA may end, whoever gave up on it.
+        for (int t = 0; t < 2; ++t)
+          if (n[t] > 0) bar_wait_slow(&sm.q_full[t], 0, kDefaultWaitNs, &give_up, p.err);
+        for (int i = max(0, c - kStages); i < c; ++i)
+          bar_wait_slow(&sm.kv_full[i % kStages], (i / kStages) & 1, kDefaultWaitNs, &give_up, p.err);
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // nothing of this CTA is in flight when it ends
         int over = 0;
         mma_commit(&sm.done);
-        bar_wait_slow(&sm.done, 0, p.wait_ns, &over, p.err);
+        bar_wait_slow(&sm.done, 0, kDefaultWaitNs, &over, p.err);
       }
       __syncwarp();
     } else if (warp < 8) {

@@ -34,7 +34,8 @@ PAGED_FORMATS = {"int8": 0, "e4m3": 1}  # kvq_paged_config.format
 F16, BF16 = 0, 1  # 16-bit types of the paged cache and of the prompt attention
 PAGED_ERR_NEW, PAGED_ERR_LENGTH, PAGED_ERR_BLOCKS, PAGED_ERR_STATE = 1, 2, 4, 8  # bits of step.status[0]
 PAGED_ERR_ROWS, PAGED_ERR_TABLE = 16, 32
-PAGED_ZERO_REST, PAGED_EARLY_TABLES = 1, 2  # flag bits of kvq_paged_decode_attention
+PAGED_ZERO_REST, PAGED_EARLY_TABLES, PAGED_ZERO_WAIT_LIMIT = 1, 2, 4  # flag bits of kvq_paged_decode_attention
+PROMPT_ZERO_REST, PROMPT_ZERO_WAIT_LIMIT = 1, 2  # flag bits of kvq_prompt_args
 PAGED_ERR_NAMES = {1: "new_tokens below -1 or more than max_new in all", 2: "a request outgrows max_blocks",
                    4: "not enough free blocks", 8: "lengths or free count out of range",
                    16: "fewer key/value rows than the step's new tokens", 32: "a block number outside the pool"}
@@ -94,7 +95,7 @@ class kvq_paged_step(ctypes.Structure):
 
 
 class kvq_prompt_args(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int32) for n in ("n_kv_heads", "gqa_ratio", "d_head", "dtype", "n_seqs", "causal", "zero_rest")]
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_kv_heads", "gqa_ratio", "d_head", "dtype", "n_seqs", "causal", "flags")]
                 + [(n, ctypes.c_int64) for n in ("n_q", "n_kv")] + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
                 + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
                 + [(n, ctypes.c_void_p) for n in ("q_start", "kv_start")] + [("softmax_scale", ctypes.c_float)]

@@ -169,10 +169,10 @@ class PagedKVCache:
         return (kvq.PAGED_ZERO_REST if fresh else 0) | (kvq.PAGED_EARLY_TABLES if early else 0)
 
     def attention(self, layer: int, q: torch.Tensor, softmax_scale: float, out: torch.Tensor = None,
-                  early=None) -> torch.Tensor:
+                  early=None, flags: int = 0) -> torch.Tensor:
         """Attention of the newest token of every request in the step. q: [n_requests][n_q][d_head];
         returns out of the same shape. Rows of requests without new tokens keep what `out` held
-        (a new `out` holds zeros there)."""
+        (a new `out` holds zeros there). flags: extra bits (PAGED_ZERO_WAIT_LIMIT)."""
         c = self.cfg
         qs = _rows("q", q, self.device, self.dtype, self.n_q, c.d_head)
         if q.shape[0] != c.n_requests:
@@ -183,7 +183,7 @@ class PagedKVCache:
         elif out.shape != q.shape or out.dtype != self.dtype or out.device != self.device or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous {self.dtype} tensor of shape {tuple(q.shape)} on {self.device}")
         self._call("kvq_paged_decode_attention", self._cfg, self._bufs, self._table, self._step, layer, q.data_ptr(), qs,
-                   softmax_scale, out.data_ptr(), self._flags(fresh, early), self._ws, self.ws.numel())
+                   softmax_scale, out.data_ptr(), self._flags(fresh, early) | flags, self._ws, self.ws.numel())
         self._tables_on = None
         return out
 

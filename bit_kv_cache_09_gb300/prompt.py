@@ -33,14 +33,14 @@ class PromptAttention:
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, *,
                  softmax_scale: float, kv_start: torch.Tensor = None, causal: bool = True, out: torch.Tensor = None,
-                 return_lse: bool = False):
+                 return_lse: bool = False, flags: int = 0):
         """q: [tokens][n_q][d_head]; k, v: [tokens][n_kv][d_head] (row strides are free: views of
         a fused projection); q_start, kv_start: int32 [sequences + 1] on the device, the first row of
         each sequence and the end of the last (kv_start None: the same as q_start). With causal the
         last query of a sequence sees its last key. Returns out [tokens][n_q][d_head] and, with
         return_lse, the natural logarithm of each row's sum of exponentials, float32 [tokens][n_q]
         (rows of no sequence: zeros and -inf; an `out` that was passed without return_lse keeps
-        what it held there)."""
+        what it held there). flags: extra bits (PROMPT_ZERO_WAIT_LIMIT)."""
         qs = _rows("q", q, self.device, self.dtype, self.n_q, self.d_head)
         ks = _rows("k", k, self.device, self.dtype, self.n_kv, self.d_head)
         vs = _rows("v", v, self.device, self.dtype, self.n_kv, self.d_head)
@@ -58,7 +58,7 @@ class PromptAttention:
         os = _rows("out", out, self.device, self.dtype, self.n_q, self.d_head)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if return_lse else None
         args = kvq.kvq_prompt_args(self.n_kv, self.gqa, self.d_head, self._dtype_code, q_start.numel() - 1, causal,
-                                   fresh or return_lse, q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   (kvq.PROMPT_ZERO_REST if fresh or return_lse else 0) | flags, q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
                                    lse.data_ptr() if return_lse else None)
         _launch(self.device, "kvq_prompt_attention", ctypes.byref(args), self._ws, self._ws_bytes)

@@ -427,15 +427,21 @@ size_t kvq_paged_workspace_size(const kvq_paged_config* cfg);
  * flags: KVQ_PAGED_ZERO_REST fills those rows with zeros. KVQ_PAGED_EARLY_TABLES lets the kernel
  * read step.lens, step.tile_start and block_table while the kernel just before it on `stream` runs
  * its last thread blocks; the caller guarantees that this one writes none of them (kernels before
- * it have finished by then). Other bits: KVQ_ERR_INVALID_ARG. */
+ * it have finished by then). KVQ_PAGED_ZERO_WAIT_LIMIT gives the bounded waits for tiles a limit
+ * of 0, as KVQ_DECODE_ZERO_WAIT_LIMIT does: the outputs of that call are undefined. Other bits:
+ * KVQ_ERR_INVALID_ARG. */
 #define KVQ_PAGED_ZERO_REST 1u
 #define KVQ_PAGED_EARLY_TABLES 2u
+#define KVQ_PAGED_ZERO_WAIT_LIMIT 4u
 kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_paged_buffers* bufs,
                                       const int32_t* block_table, const kvq_paged_step* step, int32_t layer,
                                       const void* q, int64_t q_stride, float softmax_scale, void* out,
                                       uint32_t flags, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- Attention of whole prompts, packed one behind the other ------------------------- */
+
+#define KVQ_PROMPT_ZERO_REST 1u /* flag bits; others: KVQ_ERR_INVALID_ARG */
+#define KVQ_PROMPT_ZERO_WAIT_LIMIT 2u
 
 /* Sequence s has queries q_start[s] .. q_start[s+1] - 1 and keys kv_start[s] ..
  * kv_start[s+1] - 1 (device arrays of n_seqs + 1, not decreasing, within the rows given;
@@ -444,7 +450,8 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
  * zeros and lse -inf. Element (token, head, c) of q, k, v and out is at token * stride +
  * head * d_head + c; strides are multiples of 8 elements, at least a row of heads and below
  * 2^31, pointers 16-byte aligned, and out and lse rows that belong to no sequence are left as they were (with
- * zero_rest != 0: filled with zeros, lse -inf). Whatever one sequence holds, it never reaches the
+ * KVQ_PROMPT_ZERO_REST: filled with zeros, lse -inf).
+ * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT. Whatever one sequence holds, it never reaches the
  * outputs of another. Within a causal sequence an infinity or NaN among the values (not the
  * keys) may reach queries up to 127 tokens before it, whose weight for it is 0.
  * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
@@ -454,7 +461,7 @@ typedef struct {
   int32_t dtype;  /* KVQ_F16 or KVQ_BF16: q, k, v and out */
   int32_t n_seqs;
   int32_t causal;
-  int32_t zero_rest;
+  uint32_t flags; /* KVQ_PROMPT_* */
   int64_t n_q, n_kv;                                /* rows of q / out / lse, rows of k / v */
   const void *q, *k, *v;
   int64_t q_stride, k_stride, v_stride, out_stride; /* elements from one token to the next */

@@ -484,6 +484,21 @@ def test_decode_queries_are_a_view_and_large_or_small():
     assert (np.abs(got - v[best, 0]) <= 2.0 ** -8 * np.abs(v[best, 0]) + 2.0 ** -24).all()
 
 
+@pytest.mark.parametrize("lens", [[3000, 40, 1, 700], [20000, 1, 1, 1]])
+def test_a_wait_that_runs_out_is_reported(lens):
+    """Every wait gives up at once: the error word says so, and the next call is right."""
+    rng = np.random.default_rng(20)
+    cache = make(n_kv_heads=4, n_blocks=sum(lens) // 32 + 4, max_blocks=max(lens) // 32 + 1, max_new=sum(lens))
+    held, _ = fill(cache, rng, lens)
+    q = rows(rng, 4, 16, torch.float16, 0.3)
+    cache.attention(0, q, SCALE, flags=kvq.PAGED_ZERO_WAIT_LIMIT)
+    with pytest.raises(kvq.KVQDeviceError) as e:
+        cache.check_errors()
+    assert e.value.word == kvq.DECODE_ERR_WAIT_TIMEOUT
+    check_rows(cache.attention(0, q, SCALE), q, held, 4, SCALE, torch.float16)
+    cache.check_errors()
+
+
 # ---- streams, graphs, together ---------------------------------------------------------------------------------
 
 def test_two_caches_on_two_streams():

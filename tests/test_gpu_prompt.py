@@ -13,6 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from bit_kv_cache_09_gb300 import build as kvq_build  # noqa: E402
+from bit_kv_cache_09_gb300 import kvq  # noqa: E402
 from bit_kv_cache_09_gb300.prompt import PromptAttention  # noqa: E402
 from paged_reference import attention, lse_tolerance, tolerance  # noqa: E402
 
@@ -223,6 +224,22 @@ def test_streams_and_graph():
         graph.replay()
         assert torch.equal(out, att(q, k, v, s, softmax_scale=SCALE))
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n,m", [(20, 20), (700, 700), (40, 9000)])
+def test_a_wait_that_runs_out_is_reported(n, m):
+    """Every wait gives up at once: the error word says so, and the next call is right."""
+    rng = np.random.default_rng(14)
+    q, k, v = rows(rng, n, 8, torch.float16), rows(rng, m, 2, torch.float16), rows(rng, m, 2, torch.float16)
+    att = PromptAttention(n_kv_heads=2, gqa_ratio=4)
+    args = dict(kv_start=starts([m]), softmax_scale=SCALE)
+    att(q, k, v, starts([n]), flags=kvq.PROMPT_ZERO_WAIT_LIMIT, **args)
+    with pytest.raises(kvq.KVQDeviceError) as e:
+        att.check_errors()
+    assert e.value.word == kvq.DECODE_ERR_WAIT_TIMEOUT
+    out = att(q, k, v, starts([n]), **args)
+    check(out, None, q, k, v, [n], [m], True, SCALE, 4, some=20)
+    att.check_errors()
 
 
 def test_refusals_of_the_caller():

@@ -107,7 +107,7 @@ def test_decode_refusals(lib):
     assert dec(c=cfg(block_tokens=256)) == 2 and dec(b=_bufs(None)) == 1 and dec(table=4097) == 1
     assert dec(sp=_step(tile_start=None)) == 1 and dec(layer=7) == 1 and dec(q=4104) == 1 and dec(out=None) == 1
     assert dec(qs=1020) == 1 and dec(scale=float("nan")) == 1 and dec(scale=float("inf")) == 1
-    assert dec(flags=4) == 1 and dec(flags=2 ** 31) == 1
+    assert dec(flags=8) == 1 and dec(flags=2 ** 31) == 1
     assert dec(ws=None) == 4 and dec(ws=4112) == 4 and dec(n=need - 1) == 4
 
 
@@ -116,13 +116,14 @@ def test_prompt_refusals(lib):
     assert need > 1024
 
     def call(ws=4096, n=need, **kw):
-        f = dict(n_kv_heads=2, gqa_ratio=4, d_head=128, dtype=0, n_seqs=1, causal=1, zero_rest=0, n_q=10, n_kv=10,
+        f = dict(n_kv_heads=2, gqa_ratio=4, d_head=128, dtype=0, n_seqs=1, causal=1, flags=0, n_q=10, n_kv=10,
                  q=4096, k=4096, v=4096, q_stride=1024, k_stride=256, v_stride=256, out_stride=1024, q_start=4096,
                  kv_start=4096, softmax_scale=0.1, out=4096, lse=None)
         f.update(kw)
         return lib.kvq_prompt_attention(B(kvq.kvq_prompt_args(*f.values())), ws, n, None)
 
     assert call(d_head=64) == 2 and call(gqa_ratio=9) == 2 and call(n_kv_heads=0) == 1 and call(n_kv_heads=256) == 2
+    assert call(flags=4) == 1 and call(flags=2 ** 31) == 1
     assert call(dtype=3) == 1 and call(causal=2) == 1 and call(n_seqs=0) == 1 and call(n_seqs=65536) == 2
     assert call(n_q=-1) == 1 and call(n_kv=2 ** 31) == 2 and call(softmax_scale=-0.1) == 1
     assert call(softmax_scale=float("nan")) == 1 and call(softmax_scale=float("inf")) == 1
