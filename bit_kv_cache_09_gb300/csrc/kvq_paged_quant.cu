@@ -8,6 +8,11 @@
 // row is read once and each code written once.
 //
 // Quotients are binary32, rounded to nearest (this file is compiled with -fmad=false).
+//
+// Both kernels are bound by HBM in principle: 768 bytes per token and head for the append, 1280 for the
+// read back. Measured on GB300, 32.8 k tokens of 24 prompts, 8 heads: append 48 us (4.2 TB/s; 58 % of
+// the issue slots are busy, about five instructions per two entries go into the exact quotient), read
+// back 60 us (5.6 TB/s, four fifths of it writes).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 

@@ -14,6 +14,11 @@
 // A softmax thread owns one row, so maxima and sums need no exchange. The running maximum
 // only moves (and O is only rescaled) when a row's maximum grew by more than 2^8: weights
 // stay below 2^15, within binary16.
+//
+// Measured on GB300, 8 kv heads of 4 query heads: 8192 tokens 340 us (1.6 PFLOP/s); a key tile takes
+// 2500 cycles for both query tiles against 2048 of the products alone, a CTA 12 k cycles to start and
+// to end. Leaving the exponentials out altogether changes 351 us to 348: the products set the pace.
+// Their operands in shared memory do too: S reads 128 bytes a cycle.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -785,7 +790,8 @@ cudaError_t launch_prompt(const PromptParams& p, int dtype, cudaStream_t stream)
   // pairs of tiles: one per 2 * tokens tokens of a sequence, at least one for a sequence with a token
   const int64_t ctas = (p.n_q / (2 * tokens) + std::min(p.n_q, p.n_seqs)) * (int64_t)p.H;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  // Few query rows over many keys: one item per CTA would leave SMs idle. The items are counted on the
+  // Few query rows over many keys: one item per CTA would leave SMs idle (8 kv heads, 32 queries over
+  // 32768 keys: 317 us whole, 78 split; 128 over 65536: 675 and 146). The items are counted on the
   // device; here only what they cannot exceed is known.
   if (ctas <= kPromptSplit && p.n_seqs <= 32 && p.n_kv >= 2 * kPartTiles * kTile)
     return dtype == KVQ_BF16 ? launch<true, true>(p, kPromptSplit, q, k, v, stream)
