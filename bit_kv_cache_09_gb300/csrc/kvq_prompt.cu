@@ -15,7 +15,7 @@
 // only moves (and O is only rescaled) when a row's maximum grew by more than 2^8: weights
 // stay below 2^15, within binary16.
 //
-// Measured on GB300, 8 kv heads of 4 query heads: 8192 tokens 340 us (1.6 PFLOP/s); a key tile takes
+// Measured on GB300, 8 kv heads of 4 query heads: 8192 tokens 347 us (1.58 PFLOP/s); a key tile takes
 // 2500 cycles for both query tiles against 2048 of the products alone, a CTA 12 k cycles to start and
 // to end. Leaving the exponentials out altogether changes 351 us to 348: the products set the pace.
 // Their operands in shared memory do too: S reads 128 bytes a cycle.
@@ -37,10 +37,10 @@ constexpr int kTile = 128;                    // query rows of a tile, keys of a
 constexpr int kPanel = kTile * 128;           // bytes: 128 rows of 64 channels, 128-byte swizzle
 constexpr int kTileBytes2 = 2 * kPanel;       // a 128 x 128 tile: two panels
 constexpr int kStages = 5;
-constexpr int kThreads = 384;                 // 2 x 4 softmax warps; MMA warp, TMA warp and two that idle
+constexpr int kThreads = 384;                 // 2 x 4 softmax warps; MMA warp, TMA warp and two that look at values
 // Registers of a thread: 168 at launch (384 x 168 = 64512); the softmax warps take 208, the
 // last four give theirs back (8 x 32 x 208 + 4 x 32 x 88 = 64512).
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kScanWarp = 10;
 constexpr int kMaxParts = 16;                 // CTAs of a split item
 constexpr int kPartTiles = 8;                 // key tiles of a part, at least
 constexpr int kPartFloats = kTile * (kDim + 2);  // of one tile's part: o [128][128], m [128], l [128]
@@ -60,7 +60,7 @@ struct Smem {
   uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_half[2], p_ready[2], o_full[2], done;
   uint32_t tmem;
   Span span;
-  int found, tile, h, part, parts, abort, last;
+  int found, tile, h, part, parts, abort, last, spoiled;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -368,6 +368,64 @@ __device__ __forceinline__ void join_rows(const PromptParams& p, const Span& sp,
   }
 }
 
+// Whether a value that some row of the pair of tiles sees and another does not, or one behind the
+// last key in the last 16 of the value product, is not finite: its weight of 0 would make the
+// other row's sums NaN. By warp w of n, from the rows in memory (at most 271 of 256 bytes, some
+// 1 % of what a long item reads; 341 -> 347 us for 8192 tokens, 54.4 -> 56.7 for 12 ragged prompts).
+template <bool BF16>
+__device__ __forceinline__ bool spoiled_values(const PromptParams& p, const Span& sp, int h, int t0, int tokens, int w, int n) {
+  const int lane = threadIdx.x & 31, shift = sp.lk - sp.lq;
+  const int from = min(max(t0 + 1 + shift, 0), sp.lk), last = min(max(min(sp.lq, t0 + 2 * tokens) + shift, 0), sp.lk);
+  const int to = min(sp.lk, (last + 15) & ~15);
+  uint32_t top = 0u;
+#pragma unroll 4
+  for (int key = from + w * 2 + (lane >> 4); key < to; key += 2 * n) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p.v + (int64_t)(sp.k0 + key) * p.v_stride + h * kDim + (lane & 15) * 8);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+  }
+  return __any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= (BF16 ? 0x7f80u : 0x7c00u));
+}
+
+// One row of the pair (0 .. 255) by one warp, a key at a time over those it sees: for items with
+// spoiled values only, where the products of whole tiles cannot tell 0 from nothing.
+template <bool BF16>
+__device__ __forceinline__ void row_by_row(const PromptParams& p, const Span& sp, int h, int t0, int tokens, int row) {
+  const int lane = threadIdx.x & 31, t = row / kTile, in = row % kTile;
+  const int token = t0 + t * tokens + in / p.r, head = h * p.r + in % p.r;
+  if (in >= tokens * p.r || token >= sp.lq) return;
+  const int see = min(max(token + 1 + sp.lk - sp.lq, 0), sp.lk);
+  if (see == 0) return;
+  auto four = [&](const uint16_t* x) {
+    const uint2 w = *reinterpret_cast<const uint2*>(x + lane * 4);
+    const uint32_t u[2] = {w.x, w.y};
+    float2 f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      f[i] = BF16 ? make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u))
+                  : __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    return make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  };
+  const int64_t at = sp.q0 + token;
+  const float4 q = four(p.q + at * p.q_stride + head * kDim);
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int j = 0; j < see; ++j) {
+    const float4 k = four(p.k + (int64_t)(sp.k0 + j) * p.k_stride + h * kDim), v = four(p.v + (int64_t)(sp.k0 + j) * p.v_stride + h * kDim);
+    float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+    s *= p.scale_log2;
+    const float mn = fmaxf(m, s), a = exp2_fast(m - mn), e = exp2_fast(s - mn);
+    m = mn;
+    l = l * a + e;
+    o = make_float4(o.x * a + e * v.x, o.y * a + e * v.y, o.z * a + e * v.z, o.w * a + e * v.w);
+  }
+  const float inv = 1.0f / l;
+  *reinterpret_cast<uint2*>(p.out + at * p.out_stride + head * kDim + lane * 4) =
+      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+}
+
 // SPLIT: items may be split along the keys (a template parameter: with the join in it the kernel for
 // whole items takes 361 instead of 342 us for 8192 tokens of 32 heads).
 template <bool BF16, bool SPLIT>
@@ -392,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bar_init(&sm.done, 1);
     sm.abort = 0;
+    sm.spoiled = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kTmaWarp && lane < 3) {
@@ -464,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp >= kScanWarp && p.causal) {
+      const Span all{sp.q0, sp.lq, sp.k0 - first_key, see_all};
+      if (spoiled_values<BF16>(p, all, h, t0, tokens, warp - kScanWarp, 2) && lane == 0) sm.spoiled = 1;
+    }
     if (warp == kTmaWarp) {
       if (elect_one() && n_max > 0) {
         int c = 0, give_up = 0;  // key and value tiles sent for
@@ -722,7 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (sm.last && warp < 8) {  // the warps that have the registers for it
       const int t0 = sm.tile * 2 * tokens;
       for (int r0 = warp * 4; r0 < 2 * kTile; r0 += 32) join_rows<BF16>(p, sp, h, t0, tokens, first_slot, parts, r0);
+      __syncwarp();
     }
+  }
+  // (parts of a split item: by the CTA that joined them)
+  if (sm.spoiled && warp < 8 && (parts == 1 || (SPLIT && parts > 1 && sm.last))) {
+    const int t0 = sm.tile * 2 * tokens;
+#pragma unroll 1
+    for (int row = warp; row < 2 * kTile; row += 8) row_by_row<BF16>(p, sm.span, h, t0, tokens, row);
   }
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }

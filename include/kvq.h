@@ -451,9 +451,8 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
  * head * d_head + c; strides are multiples of 8 elements, at least a row of heads and below
  * 2^31, pointers 16-byte aligned, and out and lse rows that belong to no sequence are left as they were (with
  * KVQ_PROMPT_ZERO_REST: filled with zeros, lse -inf).
- * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT. Whatever one sequence holds, it never reaches the
- * outputs of another. Within a causal sequence an infinity or NaN among the values (not the
- * keys) may reach queries up to 127 tokens before it, whose weight for it is 0.
+ * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT. Keys and values that a query does not see
+ * never reach its output, whatever they are (infinities and NaN too), nor does another sequence.
  * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
  * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale finite and >= 0. */
 typedef struct {

@@ -188,6 +188,34 @@ def test_split_work_keeps_nan_and_masked_rows():
     assert torch.isnan(out[5, 2]).all() and torch.isfinite(out[:5]).all() and torch.isfinite(out[6:]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,m,r", [(70, 70, 4), (300, 300, 1), (513, 700, 8), (40, 4100, 4), (130, 100, 2)])
+def test_values_behind_a_query_do_not_reach_it(n, m, r, dtype):
+    """Causal: infinities and NaN among the keys and values that a query does not see yet."""
+    rng = np.random.default_rng(15)
+    q, k, v = rows(rng, n, 2 * r, dtype), rows(rng, m, 2, dtype), rows(rng, m, 2, dtype)
+    att = PromptAttention(n_kv_heads=2, gqa_ratio=r, dtype=dtype)
+    args = dict(kv_start=starts([m]), softmax_scale=SCALE, return_lse=True)
+    want, wl = att(q, k, v, starts([n]), **args)
+    for at in sorted({m - 1, m - 2, max(m - 17, 0), max(m - n // 2, 0), max(m - n + 1, 0)}):
+        first = max(n - m + at, 0)  # the first query that sees key `at`
+        for value in (math.nan, math.inf):
+            v2 = v.clone()
+            v2[at, 0, 5] = value
+            got, gl = att(q, k, v2, starts([n]), **args)
+            check(got[:first], gl[:first], q[:first], k[:at], v[:at], [first], [at], True, SCALE, r, some=12)
+            assert not torch.isfinite(got[first:, :r, 5]).any()
+            clean = torch.ones(128, dtype=torch.bool)
+            clean[5] = False
+            assert torch.isfinite(got[:, r:]).all() and torch.isfinite(got[:, :, clean.cuda()]).all()
+            assert torch.equal(got[:, r:], want[:, r:]) and torch.equal(gl, wl)
+        k2 = k.clone()
+        k2[at, 1] = math.nan
+        got, gl = att(q, k2, v, starts([n]), **args)
+        assert torch.equal(got[:first], want[:first]) and torch.equal(gl[:first], wl[:first])
+        assert torch.isnan(got[first:, r:]).all() and torch.equal(got[:, :r], want[:, :r])
+
+
 def test_bad_starts_do_not_leave_the_rows():
     """Starts beyond the rows or decreasing are clamped: outputs are unspecified there, the other rows stand."""
     rng = np.random.default_rng(10)
