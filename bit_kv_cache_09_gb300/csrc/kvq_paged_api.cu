@@ -202,6 +202,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   if (a->n_q > 1 && (a->q_stride < nq * 128 || a->out_stride < nq * 128)) return KVQ_ERR_INVALID_ARG;  // rows overlap
   if (a->n_kv > 1 && (a->k_stride < a->n_kv_heads * 128 || a->v_stride < a->n_kv_heads * 128)) return KVQ_ERR_INVALID_ARG;
   if (a->n_q > 0 && (!aligned(a->q, 16) || !aligned(a->out, 16))) return KVQ_ERR_INVALID_ARG;
+  if (a->n_q > 0 && (a->out == a->q || (a->n_kv > 0 && (a->out == a->k || a->out == a->v)))) return KVQ_ERR_INVALID_ARG;
   if (a->n_kv > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return KVQ_ERR_INVALID_ARG;
   if (a->lse && !aligned(a->lse, 4)) return KVQ_ERR_INVALID_ARG;
   if (!aligned(ws, 256) || ws_bytes < kvq::prompt_workspace_bytes()) return KVQ_ERR_WORKSPACE;

@@ -447,12 +447,13 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
  * kv_start[s+1] - 1 (device arrays of n_seqs + 1, not decreasing, within the rows given;
  * kv_start may be the same array). With causal != 0 the last query of a sequence sees its
  * last key, the query before it one key less, and so on; a query that sees no key gets
- * zeros and lse -inf. Element (token, head, c) of q, k, v and out is at token * stride +
- * head * d_head + c; strides are multiples of 8 elements, at least a row of heads and below
- * 2^31, pointers 16-byte aligned, and out and lse rows that belong to no sequence are left as they were (with
- * KVQ_PROMPT_ZERO_REST: filled with zeros, lse -inf).
- * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT. Keys and values that a query does not see
- * never reach its output, whatever they are (infinities and NaN too), nor does another sequence.
+ * zeros and lse -inf. Keys and values that a query does not see never reach its output,
+ * whatever they are (infinities and NaN too), nor does another sequence.
+ * Element (token, head, c) of q, k, v and out is at token * stride + head * d_head + c;
+ * strides are multiples of 8 elements, at least a row of heads and below 2^31; pointers are
+ * 16-byte aligned; out overlaps none of the others. Rows of out and lse that belong to no
+ * sequence are left as they were (with KVQ_PROMPT_ZERO_REST: zeros, lse -inf).
+ * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT.
  * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
  * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale finite and >= 0. */
 typedef struct {

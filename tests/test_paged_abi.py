@@ -118,7 +118,7 @@ def test_prompt_refusals(lib):
     def call(ws=4096, n=need, **kw):
         f = dict(n_kv_heads=2, gqa_ratio=4, d_head=128, dtype=0, n_seqs=1, causal=1, flags=0, n_q=10, n_kv=10,
                  q=4096, k=4096, v=4096, q_stride=1024, k_stride=256, v_stride=256, out_stride=1024, q_start=4096,
-                 kv_start=4096, softmax_scale=0.1, out=4096, lse=None)
+                 kv_start=4096, softmax_scale=0.1, out=65536, lse=None)
         f.update(kw)
         return lib.kvq_prompt_attention(B(kvq.kvq_prompt_args(*f.values())), ws, n, None)
 
@@ -132,6 +132,7 @@ def test_prompt_refusals(lib):
         assert call(**{name: None}) == 1 and call(**{name: 4104}) == 1
         assert call(**{name + "_stride": 1028}) == 1 and call(**{name + "_stride": -1024}) == 1
     assert call(q_stride=1016) == 1 and call(out_stride=512) == 1 and call(k_stride=128) == 1  # rows would overlap
+    assert call(out=4096) == 1 and call(q=8192, k=65536) == 1 and call(v=65536) == 1  # out is one of the inputs
     assert call(lse=4097) == 1 and call(ws=None) == 4 and call(ws=4104) == 4 and call(n=need - 1) == 4
     assert lib.kvq_prompt_attention(None, 4096, need, None) == 1
     assert call(n_q=0, q=None, out=None) == 0  # nothing to compute
