@@ -415,8 +415,9 @@ __device__ __forceinline__ void row_by_row(const PromptParams& p, const Span& sp
     float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), a = exp2_fast(m - mn), e = exp2_fast(s - mn);
+    s = p.scale_log2 == 0.0f ? 0.0f : s * p.scale_log2;
+    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn;  // scores of -inf so far: weights of 0
+    const float a = exp2_fast(m - base), e = exp2_fast(s - base);
     m = mn;
     l = l * a + e;
     o = make_float4(o.x * a + e * v.x, o.y * a + e * v.y, o.z * a + e * v.z, o.w * a + e * v.w);

@@ -216,6 +216,27 @@ def test_values_behind_a_query_do_not_reach_it(n, m, r, dtype):
         assert torch.isnan(got[first:, r:]).all() and torch.equal(got[:, :r], want[:, :r])
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_infinite_scores_next_to_spoiled_values(dtype):
+    """Rows in front of a value that is not finite: a score of -inf has weight 0 there too, and with a
+    scale of 0 infinite products count as 0."""
+    rng = np.random.default_rng(15)
+    n, r = 40, 4
+    q, k, v = rows(rng, n, 2 * r, dtype), rows(rng, n, 2, dtype), rows(rng, n, 2, dtype)
+    q[:, :, 0] = 1.0
+    att = PromptAttention(n_kv_heads=2, gqa_ratio=r, dtype=dtype)
+    low = k.clone()
+    low[0, :, 0] = -math.inf
+    spoiled = v.clone()
+    spoiled[n - 1, :, 5] = math.inf
+    for values in (v, spoiled):
+        got, lse = att(q, low, values, starts([n]), softmax_scale=SCALE, return_lse=True)
+        assert torch.isnan(got[0]).all()
+        check(got[1:n - 1], lse[1:n - 1], q[1:n - 1], k[1:n - 1], v[1:n - 1], [n - 2], [n - 2], True, SCALE, r)
+        got, lse = att(q, low, values, starts([n]), softmax_scale=0.0, return_lse=True)
+        check(got[:n - 1], lse[:n - 1], q[:n - 1], k[:n - 1], v[:n - 1], [n - 1], [n - 1], True, 0.0, r)
+
+
 def test_bad_starts_do_not_leave_the_rows():
     """Starts beyond the rows or decreasing are clamped: outputs are unspecified there, the other rows stand."""
     rng = np.random.default_rng(10)
