@@ -28,7 +28,12 @@ bool step_ok(const kvq_paged_step* s) {
 
 bool stride_ok(int64_t stride) { return stride >= 0 && stride < (int64_t(1) << 31) && stride % 8 == 0; }
 
-bool finite(float x) { return x - x == 0.0f; }
+constexpr float kLog2E = 1.4426950408889634f;
+
+bool scale_ok(float x) {  // the kernels take x * log2(e)
+  const float y = x * kLog2E;
+  return y - y == 0.0f;
+}
 
 kvq_status of(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
@@ -151,7 +156,7 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   if (st != KVQ_OK) return st;
   if (!bufs_ok(bufs) || !aligned(block_table, 4) || !step_ok(step)) return KVQ_ERR_INVALID_ARG;
   if (layer < 0 || layer >= g.L || !aligned(q, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
-  if (!stride_ok(q_stride) || !finite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if (!stride_ok(q_stride) || !scale_ok(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if (flags & ~(KVQ_PAGED_ZERO_REST | KVQ_PAGED_EARLY_TABLES | KVQ_PAGED_ZERO_WAIT_LIMIT)) return KVQ_ERR_INVALID_ARG;
   if (!aligned(ws, 256) || ws_bytes < kvq::paged_workspace_bytes(g)) return KVQ_ERR_WORKSPACE;
   kvq::PagedDecodeParams p;
@@ -168,7 +173,7 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
   p.out = static_cast<uint16_t*>(out);
   p.zero_rest = (flags & KVQ_PAGED_ZERO_REST) != 0;
   p.early = (flags & KVQ_PAGED_EARLY_TABLES) != 0;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = softmax_scale * kLog2E;
   p.codes_head = g.codes_head;
   p.tails_head = g.tails_head;
   p.H = g.H;
@@ -194,7 +199,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   if (a->d_head != 128 || a->gqa_ratio > 8 || a->n_kv_heads > 255 || a->n_seqs > 65535 || a->n_q >= kMaxRows ||
       a->n_kv >= kMaxRows)
     return KVQ_ERR_UNSUPPORTED;
-  if (!finite(a->softmax_scale) || a->softmax_scale < 0.0f) return KVQ_ERR_INVALID_ARG;
+  if (!scale_ok(a->softmax_scale) || a->softmax_scale < 0.0f) return KVQ_ERR_INVALID_ARG;
   if (!aligned(a->q_start, 4) || !aligned(a->kv_start, 4)) return KVQ_ERR_INVALID_ARG;
   if (!stride_ok(a->q_stride) || !stride_ok(a->k_stride) || !stride_ok(a->v_stride) || !stride_ok(a->out_stride))
     return KVQ_ERR_INVALID_ARG;
@@ -226,7 +231,7 @@ kvq_status kvq_prompt_attention(const kvq_prompt_args* a, void* ws, size_t ws_by
   p.r = a->gqa_ratio;
   p.causal = a->causal;
   p.zero_rest = (a->flags & KVQ_PROMPT_ZERO_REST) != 0;
-  p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = a->softmax_scale * kLog2E;
   p.err = static_cast<uint32_t*>(ws);
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kvq::kPromptTickets);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kvq::kPromptParts);

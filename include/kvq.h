@@ -423,7 +423,8 @@ size_t kvq_paged_workspace_size(const kvq_paged_config* cfg);
  * of finished blocks and the 16-bit rows of the tail. q: row i at element i * q_stride
  * (16-byte aligned, a multiple of 8), its n_kv_heads * gqa_ratio heads behind one another;
  * out [n_requests][n_kv_heads * gqa_ratio][d_head] in the config's dtype (16-byte
- * aligned). Rows of requests without new tokens are left as they were.
+ * aligned). |softmax_scale| is below 2^127. Rows of requests without new tokens are left as
+ * they were.
  * flags: KVQ_PAGED_ZERO_REST fills those rows with zeros. KVQ_PAGED_EARLY_TABLES lets the kernel
  * read step.lens, step.tile_start and block_table while the kernel just before it on `stream` runs
  * its last thread blocks; the caller guarantees that this one writes none of them (kernels before
@@ -455,7 +456,7 @@ kvq_status kvq_paged_decode_attention(const kvq_paged_config* cfg, const kvq_pag
  * sequence are left as they were (with KVQ_PROMPT_ZERO_REST: zeros, lse -inf).
  * KVQ_PROMPT_ZERO_WAIT_LIMIT: as KVQ_DECODE_ZERO_WAIT_LIMIT.
  * Supported: d_head == 128, 1 <= gqa_ratio <= 8, 1 <= n_kv_heads <= 255, 1 <= n_seqs <=
- * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale finite and >= 0. */
+ * 65535, 0 <= n_q, n_kv < 2^31 - 2^16, softmax_scale >= 0 and below 2^127. */
 typedef struct {
   int32_t n_kv_heads, gqa_ratio, d_head;
   int32_t dtype;  /* KVQ_F16 or KVQ_BF16: q, k, v and out */

@@ -106,7 +106,7 @@ def test_decode_refusals(lib):
                                        ctypes.c_float(scale), out, flags, ws, n, None))
     assert dec(c=cfg(block_tokens=256)) == 2 and dec(b=_bufs(None)) == 1 and dec(table=4097) == 1
     assert dec(sp=_step(tile_start=None)) == 1 and dec(layer=7) == 1 and dec(q=4104) == 1 and dec(out=None) == 1
-    assert dec(qs=1020) == 1 and dec(scale=float("nan")) == 1 and dec(scale=float("inf")) == 1
+    assert dec(qs=1020) == 1 and dec(scale=float("nan")) == 1 and dec(scale=float("inf")) == 1 and dec(scale=3e38) == 1
     assert dec(flags=8) == 1 and dec(flags=2 ** 31) == 1
     assert dec(ws=None) == 4 and dec(ws=4112) == 4 and dec(n=need - 1) == 4
 
@@ -127,6 +127,7 @@ def test_prompt_refusals(lib):
     assert call(dtype=3) == 1 and call(causal=2) == 1 and call(n_seqs=0) == 1 and call(n_seqs=65536) == 2
     assert call(n_q=-1) == 1 and call(n_kv=2 ** 31) == 2 and call(softmax_scale=-0.1) == 1
     assert call(softmax_scale=float("nan")) == 1 and call(softmax_scale=float("inf")) == 1
+    assert call(softmax_scale=3e38) == 1
     assert call(q_start=None) == 1 and call(kv_start=4098) == 1
     for name in ("q", "k", "v", "out"):
         assert call(**{name: None}) == 1 and call(**{name: 4104}) == 1
