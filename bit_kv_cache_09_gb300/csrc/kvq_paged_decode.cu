@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) paged_decode_kernel(const Page
         e = in[i] ? e * p.scale_log2 : -INFINITY;
         mt = fmaxf(mt, e);
       }
-      const float mn = fmaxf(m, quad_max(mt));
-      const float alpha = exp2_fast(m - mn), off = kWeightExp - mn;
+      const float mn = fmaxf(m, quad_max(mt)), base = mn == -INFINITY ? 0.0f : mn;  // scores of -inf so far: weights of 0
+      const float alpha = exp2_fast(m - base), off = kWeightExp - base;
       m = mn;
       float e[4];
 #pragma unroll

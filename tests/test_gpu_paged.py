@@ -429,6 +429,28 @@ def test_decode_nan_stays_in_its_block_and_head():
     assert torch.isnan(out[0, :4]).all() and torch.isfinite(out[0, 4:]).all() and torch.isfinite(out[1]).all()
 
 
+@pytest.mark.parametrize("requests,heads", [(2, 1), (200, 8)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_decode_a_tail_tile_of_infinite_scores(requests, heads, dtype):
+    """Scores of -inf weigh 0 also where a whole tile has no other (in a warp of its own, or in front of others)."""
+    rng = np.random.default_rng(13)
+    n = 21
+    cache = make(n_requests=requests, n_kv_heads=heads, dtype=dtype, max_new=n * requests)
+    k, v = rows(rng, n * requests, heads, dtype), rows(rng, n * requests, heads, dtype)
+    for lo, hi in ((0, 16), (16, n)):  # the first tile of the tails, then the second
+        low = k.clone().view(requests, n, heads, 128)
+        low[:, lo:hi, :, 0] = -math.inf
+        cache.step(ints([n] * requests))
+        cache.append(0, low.view(-1, heads, 128), v)
+        q = rows(rng, requests, heads * 4, dtype, 0.3)
+        q[:, :, 0] = 1.0
+        keep = np.arange(16, n) if lo == 0 else np.arange(16)
+        held = [[x.double().cpu().numpy().reshape(requests, n, heads, 128)[i, keep] for x in (k, v)] for i in range(requests)]
+        check_rows(cache.attention(0, q, SCALE), q, held, 4, SCALE, dtype)
+        cache.step(ints([-1] * requests))
+    cache.check_errors()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 def test_decode_scales(scale):
     rng = np.random.default_rng(13)
