@@ -40,7 +40,7 @@ class PromptAttention:
         last query of a sequence sees its last key. Returns out [tokens][n_q][d_head] and, with
         return_lse, the natural logarithm of each row's sum of exponentials, float32 [tokens][n_q]
         (rows of no sequence: zeros and -inf; an `out` that was passed without return_lse keeps
-        what it held there). flags: extra bits (PROMPT_ZERO_WAIT_LIMIT)."""
+        what it held there). `out` must not overlap q, k or v. flags: extra bits (PROMPT_ZERO_WAIT_LIMIT)."""
         qs = _rows("q", q, self.device, self.dtype, self.n_q, self.d_head)
         ks = _rows("k", k, self.device, self.dtype, self.n_kv, self.d_head)
         vs = _rows("v", v, self.device, self.dtype, self.n_kv, self.d_head)
@@ -58,8 +58,8 @@ class PromptAttention:
         os = _rows("out", out, self.device, self.dtype, self.n_q, self.d_head)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if return_lse else None
         args = kvq.kvq_prompt_args(self.n_kv, self.gqa, self.d_head, self._dtype_code, q_start.numel() - 1, causal,
-                                   (kvq.PROMPT_ZERO_REST if fresh or return_lse else 0) | flags, q.shape[0], k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                   qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
+                                   (kvq.PROMPT_ZERO_REST if fresh or return_lse else 0) | flags, q.shape[0],
+                                   k.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, os, qp, kp, softmax_scale, out.data_ptr(),
                                    lse.data_ptr() if return_lse else None)
         _launch(self.device, "kvq_prompt_attention", ctypes.byref(args), self._ws, self._ws_bytes)
         return (out, lse) if return_lse else out
